@@ -623,3 +623,15 @@ def pack_for_ranks(x, topk_idx, topk_weights, num_experts: int, num_partitions: 
                             num_experts, _ptr(part), h.c, _ptr(local_idx), _ptr(local_w),
                             _stream()))
     return send_x, send_scales, local_idx, local_w, lay, part
+
+
+# ----------------------------------------------------------------------------
+# the expert layer: gate, FP8 quantisers, grouped product and weight gradient,
+# SwiGLU with an 8-bit checkpoint
+# ----------------------------------------------------------------------------
+
+from .experts import (  # noqa: E402
+    EP_GATE_SIGMOID, EP_GATE_SOFTMAX, Fp8Weights, Gate, ep_gate, ep_gate_backward,
+    ep_gate_workspace_bytes, ep_grouped_gemm_fp8, ep_grouped_wgrad_fp8, ep_quantize_rows,
+    ep_quantize_weights, ep_swiglu_fp8, ep_swiglu_fp8_backward, gate, gate_backward, grouped_gemm_fp8,
+    grouped_wgrad_fp8, quantize_rows, quantize_weights, swiglu_fp8, swiglu_fp8_backward)

@@ -3,37 +3,21 @@
 // except ep_handle_recv_counts (a small device-to-host copy).
 #include "moe_ep.h"
 
-#include <stdarg.h>
 #include <stdio.h>
 #include <stdlib.h>
 #include <string.h>
 
 #include <mutex>
-#include <string>
 
+#include "api_check.h"
 #include "launch.h"
 
+using moe_ep::aligned;
+using moe_ep::fail;
+using moe_ep::g_err;
+using moe_ep::hip_fail;
+
 namespace {
-
-thread_local std::string g_err;
-
-int fail(int code, const char* fmt, ...)
-{
-    char buf[512];
-    va_list ap;
-    va_start(ap, fmt);
-    vsnprintf(buf, sizeof buf, fmt, ap);
-    va_end(ap);
-    g_err = buf;
-    return code;
-}
-
-int hip_fail(hipError_t e, const char* what)
-{
-    return fail(EP_EHIP, "%s: %s", what, hipGetErrorString(e));
-}
-
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 constexpr int kChunk = 256;
 constexpr size_t kAlign = 256;

@@ -122,7 +122,7 @@ typedef struct ep_handle {
 
 /* Library version, major*10000 + minor*100 + patch.  EP_VERSION is the
  * version of this header; ep_version() that of the loaded library. */
-#define EP_VERSION 10201
+#define EP_VERSION 10300
 int ep_version(void);
 
 /* Message describing the last error returned on this thread ("" if none). */
@@ -478,6 +478,155 @@ int ep_recv_counts_decode(const ep_handle_t* handle, const int32_t* host_buf,
  * codec on its own.  in: device fp32 [n]; out: device uint8 [n].
  */
 int ep_e4m3fn_encode(const float* in, uint8_t* out, int64_t n, hipStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * The expert layer between dispatch and combine, and the gate before it.
+ *
+ * Row groups.  The calls below that work on receive rows take them as groups
+ * (one per expert, num_groups in [1, EP_MAX_EXPERTS]) by four arguments:
+ *   group_offsets  device int32 [num_groups + 1]; group g holds
+ *                  group_offsets[g+1] - group_offsets[g] rows (negative: none)
+ *   group_stride   0: group g begins at row group_offsets[g] (dense and
+ *                  aligned layouts); else at row g*group_stride, and holds at
+ *                  most group_stride rows (the static layout)
+ *   num_rows       rows of the row arrays; rows at or past it do not exist
+ * For a dispatched handle they are expert_offset, num_experts, static_cap and
+ * capacity_rows.  The offsets are read on the device only (no host sync), and
+ * clamped to num_rows there.  Rows of no group are neither read nor written.
+ * The padding rows of an aligned layout count as rows of their group (dispatch
+ * wrote them as zeros).  Widths are multiples of 128, at most EP_MAX_HIDDEN.
+ * FP8 rows are E4M3FN codes [num_rows][width] with fp32 scales, one per row and
+ * 128 channels: scale_ld 0: [num_rows][width/128]; else [width/128][scale_ld],
+ * scale_ld >= num_rows and a multiple of 4.  Code and bf16 arrays are 16-byte
+ * aligned, the others 4-byte (int64: 8-byte).
+ * ------------------------------------------------------------------------- */
+
+#define EP_GATE_SOFTMAX 0
+#define EP_GATE_SIGMOID 1
+
+/*
+ * The gate: top-K experts of every token with their weights, the pairs per
+ * expert and the balance loss.
+ *   score     SOFTMAX: p = softmax(l), r = p;  SIGMOID: r = 1/(1+e^-l), p = r / sum r
+ *   choice    the K largest logits, ties to the lower id, in descending order.
+ *             A logit of -inf is never chosen; a token with fewer than K others
+ *             gets id -1 and weight 0 in the places left (dispatch skips them)
+ *   weights   scale * r_k / (sum of the chosen r) if normalize, else scale * r_k
+ *   loss      balance_coef * sum_e f_e * P_e, f_e = E*n_e / (K*V),
+ *             P_e = (sum over the V tokens that count of p_te) / V; 0 when V = 0
+ * A token counts unless token_mask is 0 for it or all its logits are -inf; a
+ * masked token's logits are not looked at (they may hold anything), its ids are
+ * -1 and its weights 0.
+ *
+ *   logits                 device fp32 or (logits_bf16) bf16, row t from logits + t*ld, ld >= E
+ *   num_tokens ..          0 <= T, 1 <= E <= EP_MAX_EXPERTS, 1 <= K <= min(E, EP_MAX_TOPK)
+ *   token_mask             device uint8 [T] or NULL
+ *   topk_idx               device int64 [T*K], as the layout calls take it
+ *   topk_weights           device fp32 [T*K]
+ *   num_tokens_per_expert  device int32 [E], the n_e
+ *   num_valid              device int32 [1], V
+ *   loss                   device fp32 [1]
+ *   ws                     ep_gate_workspace_bytes(T, E) bytes, 256-byte aligned; free
+ *                          again once the call's work has run
+ * Sums over tokens are taken in an order fixed by T and E: results repeat bit
+ * for bit.  NaN logits are not chosen and make the loss NaN.
+ * Errors: EP_EINVAL, EP_EHIP.
+ */
+size_t ep_gate_workspace_bytes(int num_tokens, int num_experts);
+int ep_gate(const void* logits, int logits_bf16, int64_t ld, int num_tokens, int num_experts,
+            int num_topk, int score, int normalize, float scale, float balance_coef,
+            const uint8_t* token_mask, int64_t* topk_idx, float* topk_weights,
+            int32_t* num_tokens_per_expert, int32_t* num_valid, float* loss, void* ws,
+            size_t ws_bytes, hipStream_t stream);
+
+/*
+ * Backward of the gate, from the logits and what the forward call returned: the
+ * gradient of  sum(grad_weights * topk_weights) + grad_loss * loss  towards the
+ * logits, with the choice and the counts n_e as constants.
+ *   grad_weights  device fp32 [T*K] or NULL (zero)
+ *   grad_loss     device fp32 [1] or NULL (zero)
+ *   grad_logits   device [T*E], dense, of the logits' type; masked tokens get 0
+ * Errors: EP_EINVAL, EP_EHIP.
+ */
+int ep_gate_backward(const void* logits, int logits_bf16, int64_t ld, int num_tokens,
+                     int num_experts, int num_topk, int score, int normalize, float scale,
+                     float balance_coef, const uint8_t* token_mask, const int64_t* topk_idx,
+                     const int32_t* num_tokens_per_expert, const int32_t* num_valid,
+                     const float* grad_weights, const float* grad_loss, void* grad_logits,
+                     hipStream_t stream);
+
+/*
+ * FP8 quantisers with dispatch's arithmetic: a = max(amax, 2^-64), codes =
+ * RNE(x * (448 / a)), scale = a / 448.
+ * ep_quantize_rows: bf16 rows [num_rows][width], blocks of 1 x 128.
+ *   group_offsets may be NULL (num_groups, group_stride 0): every row.
+ * ep_quantize_weights: [G][N][K] bf16 or (w_f32) fp32, blocks of 128 x 128;
+ *   N, K multiples of 128; codes [G][N][K], scales [G][N/128][K/128].
+ *   codes_t, scales_t: NULL, or also the transposed weights [G][K][N] and
+ *   [G][K/128][N/128] (the same codes), what the product towards the input reads.
+ * Errors: EP_EINVAL, EP_EHIP.
+ */
+int ep_quantize_rows(const void* x, int width, const int32_t* group_offsets, int num_groups,
+                     int group_stride, int num_rows, int scale_ld, void* codes, float* scales,
+                     hipStream_t stream);
+int ep_quantize_weights(const void* w, int w_f32, int num_groups, int n, int k, void* codes,
+                        float* scales, void* codes_t, float* scales_t, hipStream_t stream);
+
+/*
+ * Grouped FP8 product (the grouped GEMM dispatch's counts are for): for every
+ * row r of group g
+ *   out[r][n] = bf16_rne( sum over blocks b of x_scales[r][b] * w_scales[g][n/128][b]
+ *                         * sum over k in b of x[r][k] * w[g][n][k] )
+ * The inner sums (128 exact products) and the outer ones are fp32.
+ *   x, x_scales, scale_ld   FP8 rows of width k, as dispatch wrote them
+ *   w, w_scales             as ep_quantize_weights writes them; for the gradient
+ *                           towards x, its transposed arrays with n and k swapped
+ *   expected_rows           typical rows of a group, which choose the tile (0:
+ *                           num_rows / num_groups); results do not depend on it
+ *                           but for the order of the fp32 sums
+ *   out                     device bf16 [num_rows][n]
+ * Errors: EP_EINVAL, EP_EHIP.
+ */
+int ep_grouped_gemm_fp8(const void* x, const float* x_scales, int scale_ld, const void* w,
+                        const float* w_scales, const int32_t* group_offsets, int num_groups,
+                        int group_stride, int num_rows, int n, int k, int expected_rows, void* out,
+                        hipStream_t stream);
+
+/*
+ * Grouped weight gradient, reading the product's input in the 8 bits it was
+ * kept in: out[g][n][k] = sum over the rows r of group g of
+ * grad[r][n] * bf16_rne(x[r][k] * x_scales[r][k/128]), fp32 sums; 0 for a group
+ * without rows.
+ *   grad   device bf16 [num_rows][n]
+ *   out    device bf16 (rounded once) or, with out_f32, fp32 [G][n][k]; every
+ *          group is written
+ * Errors: EP_EINVAL, EP_EHIP.
+ */
+int ep_grouped_wgrad_fp8(const void* grad, const void* x, const float* x_scales, int scale_ld,
+                         const int32_t* group_offsets, int num_groups, int group_stride,
+                         int num_rows, int n, int k, void* out, int out_f32, hipStream_t stream);
+
+/*
+ * SwiGLU between the two products: h = [g | u], bf16 [num_rows][2*inner];
+ * a = g / (1 + e^-g) * u in fp32, then quantised as rows.
+ *   codes, scales, scale_ld   a, FP8 rows of width inner
+ *   ckpt, ckpt_scales         NULL, or h itself as FP8 rows of width 2*inner
+ *                             (scales row-major): what the backward pass reads
+ * Backward, from the checkpoint's g and u:
+ *   dg = da * u * s(g) * (1 + g * (1 - s(g))), du = da * g * s(g), s(g) = 1/(1+e^-g)
+ *   grad_a         device bf16 [num_rows][inner]
+ *   grad_h         NULL, or bf16 [num_rows][2*inner], [dg | du]
+ *   codes, scales  NULL, or the same (from the fp32 values) as FP8 rows of width
+ *                  2*inner; one of grad_h and codes is given
+ * Errors: EP_EINVAL, EP_EHIP.
+ */
+int ep_swiglu_fp8(const void* h, int inner, const int32_t* group_offsets, int num_groups,
+                  int group_stride, int num_rows, int scale_ld, void* codes, float* scales,
+                  void* ckpt, float* ckpt_scales, hipStream_t stream);
+int ep_swiglu_fp8_backward(const void* grad_a, const void* ckpt, const float* ckpt_scales, int inner,
+                           const int32_t* group_offsets, int num_groups, int group_stride,
+                           int num_rows, int scale_ld, void* grad_h, void* codes, float* scales,
+                           hipStream_t stream);
 
 #ifdef __cplusplus
 }
