@@ -8,6 +8,7 @@
 // scale for them.
 #include "expert_launch.h"
 #include "mfma.h"
+#include "moe_ep.h"
 
 namespace moe_ep {
 
@@ -114,10 +115,176 @@ __global__ __launch_bounds__(256) void gemm_skinny_kernel(GemmLaunch a)
     }
 }
 
+// Large tiles: 256 rows x 256 columns by eight waves, each 64 rows x 128
+// columns (one scale block of the weights).  One K block of both operands
+// (2 x 32 KB and the rows' scales) is computed from LDS while the next one is
+// copied in behind it.  LDS rows are the 128 bytes of a K block; a row's 16-byte
+// chunks are permuted by its number, which the copy does for free (it chooses
+// which global chunk lands where), so that eight rows read at the same chunk
+// hit all banks once.
+constexpr int kTile = 256;
+constexpr int kStage = kTile * kQBlock;
+
+struct TileSource {
+    const uint8_t* x;             // first row of the tile
+    const uint8_t* w;
+    const float* xs;
+    uint32_t xo[4], wo[4], so;    // this lane's offsets from them
+};
+
+// Wave w copies rows 8 * (8 * i + w) .. + 7 of both operands; waves 0-3 the scales.
+__device__ __forceinline__ void copy_stage(const TileSource& t, int kb, uint32_t sstep, int wave, uint8_t* lx,
+                                           uint8_t* lw, float* ls)
+{
+    const uint32_t k = kb * kQBlock;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        load_to_lds16(t.w + (t.wo[i] + k), lw + (8 * i + wave) * 1024);
+        load_to_lds16(t.x + (t.xo[i] + k), lx + (8 * i + wave) * 1024);
+    }
+    if (wave < 4)
+        load_to_lds4(t.xs + (t.so + (size_t)kb * sstep), ls + wave * 64);
+}
+
+__device__ __forceinline__ i32x8 read_fragment(const uint8_t* lds, int row, int lane)
+{
+    const int c = lane >> 4, sw = row & 7;
+    const u32x4 lo = *reinterpret_cast<const u32x4*>(lds + row * kQBlock + ((c ^ sw) << 4));
+    const u32x4 hi = *reinterpret_cast<const u32x4*>(lds + row * kQBlock + (((c + 4) ^ sw) << 4));
+    return join(lo, hi);
+}
+
+// One K block: the wave's 4 row tiles x 8 column tiles.  A matrix instruction's
+// result is scaled and added three instructions later, while the next ones run;
+// the order is pinned, since left alone the compiler waits for each result.
+__device__ __forceinline__ void compute_stage(const uint8_t* lx, const uint8_t* lw, const float* ls, float sw,
+                                              int row0, int col0, int lane, f32x4 (&acc)[4][8])
+{
+    i32x8 x[4], w[3];
+    float s[4];
+    f32x4 d[4];
+    w[0] = read_fragment(lw, col0 + (lane & 15), lane);
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+        x[r] = read_fragment(lx, row0 + 16 * r + (lane & 15), lane);
+    w[1] = read_fragment(lw, col0 + 16 + (lane & 15), lane);
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+        s[r] = ls[row0 + 16 * r + (lane & 15)] * sw;
+#pragma unroll
+    for (int i = 0; i < 32 + 3; ++i) {
+        const int c = i >> 2, r = i & 3;
+        if (i < 32)
+            d[r] = mfma_fp8(w[c % 3], x[r]);
+        if (r == 0 && c + 2 < 8)
+            w[(c + 2) % 3] = read_fragment(lw, col0 + 16 * (c + 2) + (lane & 15), lane);
+        if (i >= 3) {
+            const int pc = (i - 3) >> 2, pr = (i - 3) & 3;
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                acc[pr][pc][q] = __builtin_fmaf(d[pr][q], s[pr], acc[pr][pc][q]);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+    }
+}
+
+__global__ __launch_bounds__(512, 2) void gemm_tile_kernel(GemmLaunch a)
+{
+    __shared__ __align__(1024) uint8_t lx0[kStage], lx1[kStage], lw0[kStage], lw1[kStage];
+    __shared__ __align__(1024) float ls0[kTile], ls1[kTile];
+    __shared__ float lsw[2][EP_MAX_HIDDEN / kQBlock];
+    __shared__ int prefix[EP_MAX_EXPERTS + 1];
+    const int tid = threadIdx.x, lane = tid % kWave, wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const int N = a.N, K = a.K, KB = K / kQBlock, NB = N / kQBlock, NT = (N + kTile - 1) / kTile;
+    tile_prefix<kTile>(a.groups, prefix);
+    __syncthreads();
+    const int64_t total = (int64_t)prefix[a.groups.num] * NT;
+    const int64_t per = (total + kXcds - 1) / kXcds;
+    const int xcd = blockIdx.x % kXcds;
+    const uint32_t sstep = a.x_scale_ld ? a.x_scale_ld : 1;
+    const int row0 = (wave >> 1) * 64, col0 = (wave & 1) * 128;
+    for (int64_t it = blockIdx.x / kXcds; it < per; it += gridDim.x / kXcds) {
+        const int64_t t = xcd * per + it;
+        if (t >= total)
+            break;
+        const int g = __builtin_amdgcn_readfirstlane(find_group(prefix, a.groups.num, t, NT));
+        int begin, end;
+        group_bounds(a.groups, g, begin, end);
+        const int mt = prefix[g + 1] - prefix[g];
+        const int local = (int)(t - (int64_t)prefix[g] * NT);
+        const int m0 = __builtin_amdgcn_readfirstlane(begin + (local % mt) * kTile);
+        const int n0 = __builtin_amdgcn_readfirstlane((local / mt) * kTile);
+        TileSource src;
+        src.x = a.x + (size_t)m0 * K;
+        src.w = a.w + ((size_t)g * N + n0) * K;
+        src.xs = a.x_scales + scale_at(m0, 0, KB, a.x_scale_ld);
+        const int last_row = end - 1 - m0, last_col = N - 1 - n0;   // rows past the end: the last one again
+        const int chunk = ((lane & 7) ^ (lane >> 3)) * 16;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = (8 * i + wave) * 8 + (lane >> 3);
+            src.xo[i] = (uint32_t)min(r, last_row) * K + chunk;
+            src.wo[i] = (uint32_t)min(r, last_col) * K + chunk;
+        }
+        {
+            const int r = min((wave & 3) * 64 + lane, last_row);
+            src.so = a.x_scale_ld ? r : (uint32_t)r * KB;
+        }
+        const bool on = row0 <= last_row && col0 <= last_col;
+        for (int i = tid; i < 2 * KB; i += 512) {
+            const int half = i >= KB, nb = min(n0 / kQBlock + half, NB - 1);
+            lsw[half][i - half * KB] = a.w_scales[((size_t)g * NB + nb) * KB + i - half * KB];
+        }
+        const float* sw = lsw[wave & 1];
+        f32x4 acc[4][8];
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+                acc[r][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        copy_stage(src, 0, sstep, wave, lx0, lw0, ls0);
+        __syncthreads();
+        for (int kb = 0; kb < KB; kb += 2) {
+            if (kb + 1 < KB)
+                copy_stage(src, kb + 1, sstep, wave, lx1, lw1, ls1);
+            if (on)
+                compute_stage(lx0, lw0, ls0, sw[kb], row0, col0, lane, acc);
+            __syncthreads();
+            if (kb + 1 < KB) {
+                if (kb + 2 < KB)
+                    copy_stage(src, kb + 2, sstep, wave, lx0, lw0, ls0);
+                if (on)
+                    compute_stage(lx1, lw1, ls1, sw[kb + 1], row0, col0, lane, acc);
+                __syncthreads();
+            }
+        }
+        if (on) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int row = row0 + 16 * r + (lane & 15);
+                if (row > last_row)
+                    continue;
+                uint16_t* o = a.out + (size_t)(m0 + row) * N + n0 + col0 + 4 * (lane >> 4);
+#pragma unroll
+                for (int c = 0; c < 8; ++c)
+                    *reinterpret_cast<uint2*>(o + 16 * c) =
+                        uint2{pack_bf16x2(acc[r][c][0], acc[r][c][1]), pack_bf16x2(acc[r][c][2], acc[r][c][3])};
+            }
+        }
+        // the last barrier lies behind every read of lsw and the stages: the next tile may overwrite them
+    }
+}
+
 hipError_t launch_grouped_gemm(const GemmLaunch& L, hipStream_t stream)
 {
     if (L.groups.rows == 0 || L.groups.num == 0)
         return hipSuccess;
+    if (L.expected_rows > 96) {
+        const dim3 grid(256);
+        debug_launch("grouped_gemm_tile", grid, dim3(512), 0);
+        gemm_tile_kernel<<<grid, 512, 0, stream>>>(L);
+        return hipGetLastError();
+    }
     const size_t lds = (size_t)(L.groups.num + 1) * 4;
     const dim3 grid(256 * 4);
     debug_launch("grouped_gemm_skinny", grid, dim3(256), lds);
