@@ -12,7 +12,7 @@
 
 namespace moe_ep {
 
-constexpr int kXcds = 8;
+constexpr int kXcds = 8, kCus = 256;
 
 // Skinny tiles, for few rows a group: a workgroup's four waves split the K
 // blocks of a 16*RT x 16*CT tile between them (operands straight from memory to
@@ -109,7 +109,7 @@ __global__ __launch_bounds__(256) void gemm_skinny_kernel(GemmLaunch a)
             const int row = m0 + 16 * r + (lane & 15);
             if (row < end)
                 *reinterpret_cast<uint2*>(a.out + (size_t)row * N + n0 + 16 * c + 4 * (lane >> 4)) =
-                    uint2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+                    uint2{pack2_bf16(v[0], v[1]), pack2_bf16(v[2], v[3])};
         }
         __syncthreads();
     }
@@ -122,19 +122,30 @@ __global__ __launch_bounds__(256) void gemm_skinny_kernel(GemmLaunch a)
 // chunks are permuted by its number, which the copy does for free (it chooses
 // which global chunk lands where), so that eight rows read at the same chunk
 // hit all banks once.
+//
+// 65536 rows in 32 groups, N = 4096, K = 7168: 1865 us, 2.07 PFLOP/s, where a library
+// product of E4M3 matrices with one scale reaches 2.9 (8192^3) to 3.2 (16384^3).  The
+// matrix cores are busy for half of the time.  Taken apart: the copies alone
+// take 1320-1400 us (two stages in flight; 1830 us with one, as here, when nothing is
+// computed meanwhile), the matrix instructions and scaled sums alone 1290 us, with
+// the LDS reads 1390 us; together they do not overlap fully, and the clock falls with
+// the load (2.4 GHz to 2.0).  Forms with a stream of stages across tiles, copies one
+// and a half stages ahead, or pinned fetches into L2 came out within 3% or slower.
 constexpr int kTile = 256;
 constexpr int kStage = kTile * kQBlock;
 
+// Where a tile's operands come from, and this lane's offsets.  Wave w copies rows
+// 8 * (8 * i + w) .. + 7 of both operands.
 struct TileSource {
     const uint8_t* x;             // first row of the tile
     const uint8_t* w;
     const float* xs;
-    uint32_t xo[4], wo[4], so;    // this lane's offsets from them
+    uint32_t xo[4], wo[4], so;
+    int sld;                      // column-major scales: elements between blocks
+    bool four;                    // row-major scales whose rows are whole, aligned fours
 };
 
-// Wave w copies rows 8 * (8 * i + w) .. + 7 of both operands; waves 0-3 the scales.
-__device__ __forceinline__ void copy_stage(const TileSource& t, int kb, uint32_t sstep, int wave, uint8_t* lx,
-                                           uint8_t* lw, float* ls)
+__device__ __forceinline__ void copy_stage(const TileSource& t, int kb, int wave, uint8_t* lx, uint8_t* lw)
 {
     const uint32_t k = kb * kQBlock;
 #pragma unroll
@@ -142,8 +153,25 @@ __device__ __forceinline__ void copy_stage(const TileSource& t, int kb, uint32_t
         load_to_lds16(t.w + (t.wo[i] + k), lw + (8 * i + wave) * 1024);
         load_to_lds16(t.x + (t.xo[i] + k), lx + (8 * i + wave) * 1024);
     }
-    if (wave < 4)
-        load_to_lds4(t.xs + (t.so + (size_t)kb * sstep), ls + wave * 64);
+}
+
+// The rows' scales of blocks kb .. kb + 3, by waves 0-3, 64 rows each.  In row-major
+// scales every row is a cache line of its own, so the four are fetched together:
+// one by one they were a third of all requests a tile makes (1950 against 1865 us
+// at 65536 x 4096 x 7168).
+__device__ __forceinline__ void copy_scales(const TileSource& t, int kb, int KB, int wave, float* ls)
+{
+    if (wave >= 4)
+        return;
+    if (t.four) {
+        load_to_lds16(t.xs + (t.so + kb), ls + wave * 256);            // [row][block]
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {                                  // [block][row]
+            const int k = min(kb + i, KB - 1);
+            load_to_lds4(t.xs + (t.so + (t.sld ? (size_t)k * t.sld : k)), ls + i * kTile + wave * 64);
+        }
+    }
 }
 
 __device__ __forceinline__ i32x8 read_fragment(const uint8_t* lds, int row, int lane)
@@ -157,20 +185,16 @@ __device__ __forceinline__ i32x8 read_fragment(const uint8_t* lds, int row, int 
 // One K block: the wave's 4 row tiles x 8 column tiles.  A matrix instruction's
 // result is scaled and added three instructions later, while the next ones run;
 // the order is pinned, since left alone the compiler waits for each result.
-__device__ __forceinline__ void compute_stage(const uint8_t* lx, const uint8_t* lw, const float* ls, float sw,
+__device__ __forceinline__ void compute_stage(const uint8_t* lx, const uint8_t* lw, const float (&s)[4],
                                               int row0, int col0, int lane, f32x4 (&acc)[4][8])
 {
     i32x8 x[4], w[3];
-    float s[4];
     f32x4 d[4];
     w[0] = read_fragment(lw, col0 + (lane & 15), lane);
 #pragma unroll
     for (int r = 0; r < 4; ++r)
         x[r] = read_fragment(lx, row0 + 16 * r + (lane & 15), lane);
     w[1] = read_fragment(lw, col0 + 16 + (lane & 15), lane);
-#pragma unroll
-    for (int r = 0; r < 4; ++r)
-        s[r] = ls[row0 + 16 * r + (lane & 15)] * sw;
 #pragma unroll
     for (int i = 0; i < 32 + 3; ++i) {
         const int c = i >> 2, r = i & 3;
@@ -191,7 +215,7 @@ __device__ __forceinline__ void compute_stage(const uint8_t* lx, const uint8_t* 
 __global__ __launch_bounds__(512, 2) void gemm_tile_kernel(GemmLaunch a)
 {
     __shared__ __align__(1024) uint8_t lx0[kStage], lx1[kStage], lw0[kStage], lw1[kStage];
-    __shared__ __align__(1024) float ls0[kTile], ls1[kTile];
+    __shared__ __align__(16) float ls[2][4 * kTile];
     __shared__ float lsw[2][EP_MAX_HIDDEN / kQBlock];
     __shared__ int prefix[EP_MAX_EXPERTS + 1];
     const int tid = threadIdx.x, lane = tid % kWave, wave = __builtin_amdgcn_readfirstlane(tid / kWave);
@@ -199,14 +223,9 @@ __global__ __launch_bounds__(512, 2) void gemm_tile_kernel(GemmLaunch a)
     tile_prefix<kTile>(a.groups, prefix);
     __syncthreads();
     const int64_t total = (int64_t)prefix[a.groups.num] * NT;
-    const int64_t per = (total + kXcds - 1) / kXcds;
-    const int xcd = blockIdx.x % kXcds;
-    const uint32_t sstep = a.x_scale_ld ? a.x_scale_ld : 1;
     const int row0 = (wave >> 1) * 64, col0 = (wave & 1) * 128;
-    for (int64_t it = blockIdx.x / kXcds; it < per; it += gridDim.x / kXcds) {
-        const int64_t t = xcd * per + it;
-        if (t >= total)
-            break;
+    const int64_t t0 = (int64_t)(blockIdx.x % kXcds) * (gridDim.x / kXcds) + blockIdx.x / kXcds;
+    for (int64_t t = t0; t < total; t += gridDim.x) {
         const int g = __builtin_amdgcn_readfirstlane(find_group(prefix, a.groups.num, t, NT));
         int begin, end;
         group_bounds(a.groups, g, begin, end);
@@ -229,6 +248,8 @@ __global__ __launch_bounds__(512, 2) void gemm_tile_kernel(GemmLaunch a)
         {
             const int r = min((wave & 3) * 64 + lane, last_row);
             src.so = a.x_scale_ld ? r : (uint32_t)r * KB;
+            src.sld = a.x_scale_ld;
+            src.four = !a.x_scale_ld && KB % 4 == 0 && reinterpret_cast<uintptr_t>(a.x_scales) % 16 == 0;
         }
         const bool on = row0 <= last_row && col0 <= last_col;
         for (int i = tid; i < 2 * KB; i += 512) {
@@ -242,19 +263,35 @@ __global__ __launch_bounds__(512, 2) void gemm_tile_kernel(GemmLaunch a)
 #pragma unroll
             for (int c = 0; c < 8; ++c)
                 acc[r][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        copy_stage(src, 0, sstep, wave, lx0, lw0, ls0);
+        copy_stage(src, 0, wave, lx0, lw0);
+        copy_scales(src, 0, KB, wave, ls[0]);
         __syncthreads();
+        // the stage's scales are read before its copies are issued: the compiler would
+        // wait for those of a later group
+        const auto scales = [&](int kb, float (&s)[4]) {
+            const float* p = ls[(kb >> 2) & 1];
+            const int first = src.four ? (row0 + (lane & 15)) * 4 + (kb & 3) : (kb & 3) * kTile + row0 + (lane & 15);
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                s[r] = p[first + (src.four ? 64 : 16) * r] * sw[kb];
+        };
         for (int kb = 0; kb < KB; kb += 2) {
+            float s[4];
+            scales(kb, s);
             if (kb + 1 < KB)
-                copy_stage(src, kb + 1, sstep, wave, lx1, lw1, ls1);
+                copy_stage(src, kb + 1, wave, lx1, lw1);
             if (on)
-                compute_stage(lx0, lw0, ls0, sw[kb], row0, col0, lane, acc);
+                compute_stage(lx0, lw0, s, row0, col0, lane, acc);
             __syncthreads();
             if (kb + 1 < KB) {
-                if (kb + 2 < KB)
-                    copy_stage(src, kb + 2, sstep, wave, lx0, lw0, ls0);
+                scales(kb + 1, s);
+                if (kb + 2 < KB) {
+                    copy_stage(src, kb + 2, wave, lx0, lw0);
+                    if ((kb + 2) % 4 == 0)
+                        copy_scales(src, kb + 2, KB, wave, ls[((kb + 2) >> 2) & 1]);
+                }
                 if (on)
-                    compute_stage(lx1, lw1, ls1, sw[kb + 1], row0, col0, lane, acc);
+                    compute_stage(lx1, lw1, s, row0, col0, lane, acc);
                 __syncthreads();
             }
         }
@@ -268,27 +305,47 @@ __global__ __launch_bounds__(512, 2) void gemm_tile_kernel(GemmLaunch a)
 #pragma unroll
                 for (int c = 0; c < 8; ++c)
                     *reinterpret_cast<uint2*>(o + 16 * c) =
-                        uint2{pack_bf16x2(acc[r][c][0], acc[r][c][1]), pack_bf16x2(acc[r][c][2], acc[r][c][3])};
+                        uint2{pack2_bf16(acc[r][c][0], acc[r][c][1]), pack2_bf16(acc[r][c][2], acc[r][c][3])};
             }
         }
         // the last barrier lies behind every read of lsw and the stages: the next tile may overwrite them
     }
 }
 
+template <int RT, int CT>
+static void skinny_run(const GemmLaunch& L, hipStream_t stream)
+{
+    const size_t lds = (size_t)(L.groups.num + 1) * 4;
+    const dim3 grid(kCus * 4);
+    debug_launch("grouped_gemm_skinny", grid, dim3(256), lds);
+    gemm_skinny_kernel<RT, CT><<<grid, 256, lds, stream>>>(L);
+}
+
+// The tile by the typical rows m of a group.  G = 32, N = 4096, K = 7168 (940 MB of
+// weights; 188 us at the rate of a large copy), in us:
+//   m                 2     8    16    32   128   512
+//   16 x 64 skinny  142   164   227   344  1160  4420
+//   32 x 64 skinny  158   176   187   284   787  2890
+//   256 x 256       194   196   197   201   234   570
+// The 64 x 64 skinny form is for products of few large tiles, which leave CUs idle:
+// G = 8, N = 512, K = 1024 at m = 256: 15 us against 25, at 512 (32 tiles): 22 against
+// 26.  At 64 tiles both reach about 0.5 PFLOP/s.
 hipError_t launch_grouped_gemm(const GemmLaunch& L, hipStream_t stream)
 {
     if (L.groups.rows == 0 || L.groups.num == 0)
         return hipSuccess;
-    if (L.expected_rows > 96) {
-        const dim3 grid(256);
-        debug_launch("grouped_gemm_tile", grid, dim3(512), 0);
-        gemm_tile_kernel<<<grid, 512, 0, stream>>>(L);
-        return hipGetLastError();
+    const int m = L.expected_rows;
+    const int64_t tiles = (int64_t)L.groups.num * ((m + kTile - 1) / kTile) * ((L.N + kTile - 1) / kTile);
+    if (m <= 8) {
+        skinny_run<1, 4>(L, stream);
+    } else if (m <= 16) {
+        skinny_run<2, 4>(L, stream);
+    } else if (tiles < 64) {
+        skinny_run<4, 4>(L, stream);
+    } else {
+        debug_launch("grouped_gemm_tile", dim3(kCus), dim3(512), 0);
+        gemm_tile_kernel<<<kCus, 512, 0, stream>>>(L);
     }
-    const size_t lds = (size_t)(L.groups.num + 1) * 4;
-    const dim3 grid(256 * 4);
-    debug_launch("grouped_gemm_skinny", grid, dim3(256), lds);
-    gemm_skinny_kernel<2, 2><<<grid, 256, lds, stream>>>(L);
     return hipGetLastError();
 }
 

@@ -44,9 +44,13 @@ __device__ __forceinline__ bool row_in_group(const Groups& g, int r)
     return r >= g.off[0] && r < g.off[g.num];
 }
 
-// Running count of the groups' row tiles: prefix[i] = tiles of groups before i
-// (LDS, num + 1 entries).  The first wave fills it; the caller synchronises.
-template <int TILE>
+// Running count of the groups' row tiles of TILE rows: prefix[i] = tiles of groups
+// before i (LDS, num + 1 entries); WHICH: all, only the full ones, or only the
+// groups' last, partly filled ones.  The first wave fills it; the caller
+// synchronises.
+enum { kAllTiles, kFullTiles, kPartTiles };
+
+template <int TILE, int WHICH = kAllTiles>
 __device__ __forceinline__ void tile_prefix(const Groups& g, int* prefix)
 {
     if (threadIdx.x >= kWave)
@@ -60,7 +64,8 @@ __device__ __forceinline__ void tile_prefix(const Groups& g, int* prefix)
         if (base + lane < g.num) {
             int b, e;
             group_bounds(g, base + lane, b, e);
-            n = (e - b + TILE - 1) / TILE;
+            const int full = (e - b) / TILE, part = (e - b) % TILE != 0;
+            n = WHICH == kAllTiles ? full + part : WHICH == kFullTiles ? full : part;
         }
 #pragma unroll
         for (int d = 1; d < kWave; d <<= 1) {
