@@ -12,9 +12,27 @@ dispatch's backward is ep_dispatch_backward (the unit-weight combine of the
 received rows' gradients); combine's backward is ep_combine_backward
 (weight-scaled rows of grad_out, and the weight gradient when topk_weights
 requires grad).  Receive rows that no pair maps to get a zero gradient.
+``gate`` and ``experts`` do the same for the rest of an MoE layer:
+
+    g = gate(logits, K, balance_coef=1e-2)          # ids; weights and loss with gradients
+    out = experts(x, g.topk_idx, g.topk_weights, w1, w2, P)
+    (task_loss(out) + g.loss).backward()
+
+``experts`` is dispatch, the two FP8 products with SwiGLU between them, and
+combine.  It keeps its activations for the backward pass in 8 bits (the
+dispatched rows, SwiGLU's input and output), and its gradient rows are
+quantised the same way for the products towards the inputs; the quantisers are
+taken as straight-through.
+
 Only argument marshalling happens here; every step runs in the HIP kernels.
+These functions are for eager autograd: a backward pass captured into a graph
+while an eager graph of the same leaves is alive ends the process in torch, so
+``gate`` and ``experts`` refuse to be captured (the plain calls they are made of
+can be).
 """
 from __future__ import annotations
+
+import dataclasses
 
 import torch
 
@@ -22,7 +40,11 @@ from . import combine as _combine
 from . import combine_backward as _combine_backward
 from . import dispatch as _dispatch
 from . import dispatch_backward as _dispatch_backward
+from . import gate as _gate_call
+from . import gate_backward as _gate_backward
 from . import get_dispatch_layout as _get_dispatch_layout
+from . import (grouped_gemm_fp8, grouped_wgrad_fp8, quantize_rows, quantize_weights, swiglu_fp8,
+               swiglu_fp8_backward)
 
 
 class _Routing:
@@ -96,3 +118,88 @@ def combine(y, handle, topk_weights=None):
     """Combine with gradients for y and, when it requires grad, topk_weights
     (None: the weights dispatch copied, as constants)."""
     return _Combine.apply(y, topk_weights, handle)
+
+
+def _eager_only(what):
+    if torch.cuda.is_current_stream_capturing():
+        raise RuntimeError(f"{what} cannot be captured into a graph: capture the plain calls instead")
+
+
+class _Gate(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, num_topk, options, out):
+        g = _gate_call(logits.detach(), num_topk, **options)
+        out.append(g)
+        ctx.g = g
+        ctx.save_for_backward(logits)
+        ctx.mark_non_differentiable(g.topk_idx, g.num_tokens_per_expert)
+        ctx.set_materialize_grads(False)
+        return g.topk_weights, g.loss, g.topk_idx, g.num_tokens_per_expert
+
+    @staticmethod
+    def backward(ctx, grad_weights, grad_loss, *_):
+        logits, = ctx.saved_tensors
+        if grad_weights is not None:
+            grad_weights = grad_weights.contiguous()
+        if grad_loss is not None:
+            grad_loss = grad_loss.contiguous()
+        return _gate_backward(logits.detach(), ctx.g, grad_weights, grad_loss), None, None, None
+
+
+def gate(logits, num_topk: int, **options):
+    """The gate (same options) with gradients of its weights and its balance loss
+    towards the logits."""
+    _eager_only("gate")
+    kept = []
+    w, loss, _, _ = _Gate.apply(logits, num_topk, options, kept)
+    return dataclasses.replace(kept[0], topk_weights=w, loss=loss)
+
+
+class _Experts(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, topk_weights, w1, w2, layout):
+        x8, xs, h = _dispatch(x.detach().contiguous(), topk_weights.detach().contiguous(), layout, True)
+        train = any(ctx.needs_input_grad)
+        q1 = quantize_weights(w1.detach().contiguous(), transposed=train)
+        q2 = quantize_weights(w2.detach().contiguous(), transposed=train)
+        y1 = grouped_gemm_fp8(x8, xs, q1.codes, q1.scales, h)
+        a8, a_s, c8, cs = swiglu_fp8(y1, h, checkpoint=train)
+        y2 = grouped_gemm_fp8(a8, a_s, q2.codes, q2.scales, h)
+        if train:
+            ctx.handle = h
+            ctx.dtypes = w1.dtype, w2.dtype
+            ctx.save_for_backward(x8, xs, a8, a_s, c8, cs, y2, q1.codes_t, q1.scales_t, q2.codes_t, q2.scales_t)
+        return _combine(y2, h)
+
+    @staticmethod
+    def backward(ctx, grad_out):
+        x8, xs, a8, a_s, c8, cs, y2, w1t, s1t, w2t, s2t = ctx.saved_tensors
+        h = ctx.handle
+        want_x, want_w, want_1, want_2, _ = ctx.needs_input_grad
+        gy, gw = _combine_backward(grad_out.contiguous(), h, y=y2 if want_w else None)   # dispatch's copy of the weights
+        gx = g1 = g2 = None
+        if want_2:
+            g2 = grouped_wgrad_fp8(gy, a8, a_s, h, out_dtype=ctx.dtypes[1])
+        if want_x or want_1:
+            g8, gs = quantize_rows(gy, h)
+            ga = grouped_gemm_fp8(g8, gs, w2t, s2t, h)
+            gh, gh8, ghs = swiglu_fp8_backward(ga, c8, cs, h, quantize=want_x)
+            if want_1:
+                g1 = grouped_wgrad_fp8(gh, x8, xs, h, out_dtype=ctx.dtypes[0])
+            if want_x:
+                gx = _dispatch_backward(grouped_gemm_fp8(gh8, ghs, w1t, s1t, h), h)
+        return gx, (gw if want_w else None), g1, g2, None
+
+
+def experts(x, topk_idx, topk_weights, w1, w2, num_partitions: int = 1):
+    """One expert layer in FP8 with gradients for x, topk_weights, w1 and w2.
+    x: bf16 [T, H]; topk_idx, topk_weights: [T, K]; w1: bf16 or fp32 [E, 2 * I, H]
+    (gate rows, then up rows), w2: [E, H, I].  Returns bf16 [T, H].  H and I are
+    multiples of 128."""
+    _eager_only("experts")
+    E = w1.shape[0]
+    if w1.dim() != 3 or w2.dim() != 3 or w2.shape[0] != E or w1.shape[1] != 2 * w2.shape[2] or \
+            w1.shape[2] != x.shape[1] or w2.shape[1] != x.shape[1]:
+        raise ValueError(f"x [T, H], w1 [E, 2 * I, H] and w2 [E, H, I] do not fit: {list(x.shape)}, "
+                         f"{list(w1.shape)}, {list(w2.shape)}")
+    return _Experts.apply(x, topk_weights, w1, w2, _get_dispatch_layout(topk_idx, E, num_partitions))

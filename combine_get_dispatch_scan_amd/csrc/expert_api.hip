@@ -99,7 +99,7 @@ size_t ep_gate_workspace_bytes(int T, int E)
 {
     if (T < 0 || E < 1 || E > EP_MAX_EXPERTS)
         return 0;
-    return (size_t)moe_ep::gate_blocks(T, E) * (2 * E + 1) * 4;
+    return moe_ep::gate_workspace(T, E);
 }
 
 int ep_gate(const void* logits, int logits_bf16, int64_t ld, int T, int E, int K, int score,
@@ -137,9 +137,9 @@ int ep_gate(const void* logits, int logits_bf16, int64_t ld, int T, int E, int K
     L.counts = num_tokens_per_expert;
     L.num_valid = num_valid;
     L.loss = loss;
-    L.part_p = static_cast<float*>(ws);
-    L.part_n = reinterpret_cast<int32_t*>(L.part_p + (size_t)moe_ep::gate_blocks(T, E) * E);
-    const hipError_t e = moe_ep::launch_gate(L, stream);
+    L.part_p = nullptr;
+    L.part_n = L.part_v = nullptr;
+    const hipError_t e = moe_ep::launch_gate(L, ws, stream);
     return e == hipSuccess ? EP_OK : hip_fail(e, "gate launch");
 }
 

@@ -78,11 +78,12 @@ struct GateLaunch {
     int32_t* counts;          // [E]
     int32_t* num_valid;       // [1]
     float* loss;              // [1]
-    float* part_p;            // workspace: [blocks][E]
-    int32_t* part_n;          // [blocks][E + 1]
+    float* part_p;            // workgroups' sums, in the workspace (set by launch_gate)
+    int32_t* part_n;
+    int32_t* part_v;
 };
-int gate_blocks(int T, int E);
-hipError_t launch_gate(const GateLaunch& L, hipStream_t stream);
+size_t gate_workspace(int T, int E);
+hipError_t launch_gate(GateLaunch L, void* ws, hipStream_t stream);
 
 struct GateBackwardLaunch {
     const void* logits;

@@ -8,46 +8,68 @@
 //   loss     coef * sum_e f_e P_e,  f_e = E n_e / (K V),  P_e = sum_t p_te / V
 //            over the V tokens that count
 //
-// A token is held by kLanes lanes of a wave, NV values a lane, so the K rounds
-// of "largest value, then smallest id that has it" run for 64 / kLanes tokens at
-// once.  Every lane keeps the same experts from token to token: the sums of p
-// stay in its registers until the workgroup is done.  The workgroups' sums are
-// then added in their order by a second launch (or, where one workgroup holds
-// all tokens, by the first), so the loss does not depend on timing.
+// A token is held by LANES lanes of a wave, NV values a lane, so the K rounds of
+// "largest value, then smallest id that has it" run for 64 / LANES tokens at once;
+// reductions over 16 lanes are four DPP steps.  Every lane keeps the same experts
+// from token to token: the sums of p stay in its registers until the workgroup is
+// done.  The workgroups' sums are then added in their order by a second launch, so
+// the loss does not depend on timing (a few tokens take one workgroup and one launch).
+//
+// 16384 x 256 bf16 logits, top-8 (MI355X): 16.0 us and 7.4 for the second launch,
+// the backward pass 12.8.  The 19 MB they move take 4 us at the rate of a large
+// copy; the rounds' instructions bound the first, the wait for the 256 workgroups'
+// sums (512 KB by one CU) the second, the scores' exponentials and divisions the
+// backward pass.
 #include "expert_launch.h"
 
 namespace moe_ep {
 
-constexpr int kGateThreads = 256;
+constexpr int kGateThreads = 1024;      // forward, at most
 constexpr int kGateMaxBlocks = 256;
+constexpr int kBackThreads = 256;
 constexpr float kNegInf = -__builtin_inff();
 
-// Reductions over the LANES (16, 32 or 64) lanes that hold a token.
+// Reductions over the LANES (16, 32 or 64) lanes that hold a token, for all of them.
+template <int CTRL>
+__device__ __forceinline__ int dpp(int v)
+{
+    return __builtin_amdgcn_mov_dpp(v, CTRL, 0xF, 0xF, true);
+}
+
+template <int LANES, typename F>
+__device__ __forceinline__ int group_reduce(int v, const F& f)
+{
+    v = f(v, dpp<0xB1>(v));              // lane ^ 1
+    v = f(v, dpp<0x4E>(v));              // lane ^ 2
+    v = f(v, dpp<0x141>(v));             // the other four of eight (row_half_mirror)
+    v = f(v, dpp<0x140>(v));             // the other eight of sixteen (row_mirror)
+    if (LANES > 16)
+        v = f(v, __shfl_xor(v, 16));
+    if (LANES > 32)
+        v = f(v, __shfl_xor(v, 32));
+    return v;
+}
+
 template <int LANES>
 __device__ __forceinline__ float group_max(float v)
 {
-#pragma unroll
-    for (int d = 1; d < LANES; d <<= 1)
-        v = fmaxf(v, __shfl_xor(v, d));
-    return v;
+    return __int_as_float(group_reduce<LANES>(__float_as_int(v), [](int a, int b) {
+        return __float_as_int(fmaxf(__int_as_float(a), __int_as_float(b)));
+    }));
 }
 
 template <int LANES>
 __device__ __forceinline__ int group_min(int v)
 {
-#pragma unroll
-    for (int d = 1; d < LANES; d <<= 1)
-        v = min(v, __shfl_xor(v, d));
-    return v;
+    return group_reduce<LANES>(v, [](int a, int b) { return min(a, b); });
 }
 
 template <int LANES>
 __device__ __forceinline__ float group_sum(float v)
 {
-#pragma unroll
-    for (int d = 1; d < LANES; d <<= 1)
-        v += __shfl_xor(v, d);
-    return v;
+    return __int_as_float(group_reduce<LANES>(__float_as_int(v), [](int a, int b) {
+        return __float_as_int(__int_as_float(a) + __int_as_float(b));
+    }));
 }
 
 // Expert of value v of lane j: four neighbouring experts a lane and step.
@@ -93,70 +115,50 @@ __device__ __forceinline__ void load_logits(const void* logits, int64_t at, int 
     }
 }
 
-// Scores r of the token's experts and the factor that turns them into p.
-// A token without any expert left (every logit -inf) has r = 0 and p = 0.
+template <bool SIGMOID>
+__device__ __forceinline__ float score(float x, float top)
+{
+    return SIGMOID ? 1.0f / (1.0f + expf(-x)) : expf(x - top);
+}
+
+// Scores r of the token's experts (softmax: times `norm`) and norm, 1 / their sum.
+// A token without any expert left (every logit -inf) has r = 0 and norm = 0.
 template <int LANES, int NV, bool SIGMOID>
 __device__ __forceinline__ float scores(const float (&x)[NV], float top, float (&r)[NV])
 {
     float sum = 0.0f;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-        if (SIGMOID)
-            r[v] = 1.0f / (1.0f + expf(-x[v]));
-        else
-            r[v] = top == kNegInf ? 0.0f : expf(x[v] - top);
+        r[v] = !SIGMOID && top == kNegInf ? 0.0f : score<SIGMOID>(x[v], top);
         sum += r[v];
     }
     sum = group_sum<LANES>(sum);
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    const float norm = sum == 0.0f ? 0.0f : 1.0f / sum;
     if (!SIGMOID) {
 #pragma unroll
         for (int v = 0; v < NV; ++v)
-            r[v] *= inv;
-        return 1.0f;
+            r[v] *= norm;
     }
-    return inv;
+    return norm;
 }
 
-__device__ __forceinline__ void gate_finish(const GateLaunch& a, int blocks, float* lds)
+__host__ __device__ __forceinline__ int four(int E) { return (E + 3) / 4 * 4; }
+
+// Balance loss from the sums of p (lds_p) and counts (lds_n) of all tokens; every
+// thread of the workgroup calls it.
+__device__ __forceinline__ void gate_loss(const GateLaunch& a, const float* lds_p, const int* lds_n, int stripes, int ld,
+                                          int valid)
 {
-    // thread: a stripe of workgroups of one expert; LDS: [stripes][E] sums, counts
-    const int E = a.E, n = blockDim.x;
-    const int stripes = n / E < 1 ? 1 : n / E;
-    int* lds_n = reinterpret_cast<int*>(lds + (size_t)stripes * E);
-    for (int i = threadIdx.x; i < stripes * E; i += n) {
-        const int e = i % E, s = i / E;
-        float p = 0.0f;
-        int c = 0;
-#pragma unroll 8
-        for (int b = s; b < blocks; b += stripes) {
-            p += a.part_p[(size_t)b * E + e];
-            c += a.part_n[(size_t)b * (E + 1) + e];
-        }
-        lds[i] = p;
-        lds_n[i] = c;
-    }
-    __shared__ int valid;
     __shared__ float wave_sum[16];
-    if (threadIdx.x < kWave) {
-        int c = 0;
-        for (int b = threadIdx.x; b < blocks; b += kWave)
-            c += a.part_n[(size_t)b * (E + 1) + E];
-#pragma unroll
-        for (int d = 1; d < kWave; d <<= 1)
-            c += __shfl_xor(c, d);
-        if (threadIdx.x == 0)
-            valid = c;
-    }
-    __syncthreads();
+    const int E = a.E, n = blockDim.x;
     const float V = (float)valid;
     float sum = 0.0f;
     for (int e = threadIdx.x; e < E; e += n) {
         float p = 0.0f;
         int c = 0;
         for (int s = 0; s < stripes; ++s) {
-            p += lds[s * E + e];
-            c += lds_n[s * E + e];
+            p += lds_p[s * ld + e];
+            c += lds_n[s * ld + e];
         }
         a.counts[e] = c;
         if (valid > 0)
@@ -175,22 +177,65 @@ __device__ __forceinline__ void gate_finish(const GateLaunch& a, int blocks, flo
     }
 }
 
-__global__ __launch_bounds__(1024) void gate_finish_kernel(GateLaunch a, int blocks)
+// Stripes of workgroups that the second launch adds side by side: a thread takes
+// four neighbouring experts of a stripe's workgroups.
+__host__ __device__ __forceinline__ int finish_stripes(int E)
 {
-    extern __shared__ float lds[];
-    gate_finish(a, blocks, lds);
+    const int s = kGateThreads / (four(E) / 4);
+    return s > 64 ? 64 : s;
+}
+
+__global__ __launch_bounds__(kGateThreads) void gate_finish_kernel(GateLaunch a, int blocks)
+{
+    extern __shared__ __align__(16) float lds[];
+    __shared__ int valid;
+    const int ld = four(a.E), cols = ld / 4, stripes = finish_stripes(a.E);
+    int* lds_n = reinterpret_cast<int*>(lds + (size_t)stripes * ld);
+    if (threadIdx.x < stripes * cols) {
+        const int c = threadIdx.x % cols, s = threadIdx.x / cols;
+        float p[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        int n[4] = {0, 0, 0, 0};
+#pragma unroll 8
+        for (int b = s; b < blocks; b += stripes) {
+            const u32x4 dp = load16_hint<false>(a.part_p + (size_t)b * ld + 4 * c);
+            const u32x4 dn = load16_hint<false>(a.part_n + (size_t)b * ld + 4 * c);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                p[i] += __uint_as_float(dp[i]);
+                n[i] += (int)dn[i];
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            lds[s * ld + 4 * c + i] = p[i];
+            lds_n[s * ld + 4 * c + i] = n[i];
+        }
+    }
+    if (threadIdx.x < kWave) {
+        int c = 0;
+        for (int b = threadIdx.x; b < blocks; b += kWave)
+            c += a.part_v[b];
+#pragma unroll
+        for (int d = 1; d < kWave; d <<= 1)
+            c += __shfl_xor(c, d);
+        if (threadIdx.x == 0)
+            valid = c;
+    }
+    __syncthreads();
+    gate_loss(a, lds, lds_n, stripes, ld, valid);
 }
 
 template <int LANES, int NV, bool BF16, bool VEC, bool SIGMOID>
 __global__ __launch_bounds__(kGateThreads) void gate_kernel(GateLaunch a)
 {
-    constexpr int kGroups = kGateThreads / LANES;      // tokens a workgroup holds at once
-    __shared__ float sum_p[kGroups * LANES * NV];
-    __shared__ int cnt[LANES * NV];
+    constexpr int kE = LANES * NV;
+    extern __shared__ __align__(16) float sum_p[];     // [waves][kE]
+    __shared__ int cnt[kE];
     __shared__ int cnt_valid;
+    const int threads = blockDim.x, waves = threads / kWave, groups = threads / LANES;
     const int tid = threadIdx.x, j = tid % LANES, grp = tid / LANES;
     const int E = a.E, K = a.K;
-    for (int i = tid; i < LANES * NV; i += kGateThreads)
+    for (int i = tid; i < kE; i += threads)
         cnt[i] = 0;
     if (tid == 0)
         cnt_valid = 0;
@@ -199,20 +244,20 @@ __global__ __launch_bounds__(kGateThreads) void gate_kernel(GateLaunch a)
 #pragma unroll
     for (int v = 0; v < NV; ++v)
         psum[v] = 0.0f;
-    for (int t = blockIdx.x * kGroups + grp; t < a.T; t += gridDim.x * kGroups) {
+    for (int64_t t = (int64_t)blockIdx.x * groups + grp; t < a.T; t += (int64_t)gridDim.x * groups) {
         const bool masked = a.token_mask && a.token_mask[t] == 0;
         float x[NV], r[NV];
         // a masked token's logits are not looked at: they may hold anything
-        load_logits<LANES, NV, BF16, VEC>(a.logits, (int64_t)t * a.ld, masked ? 0 : E, j, x);
+        load_logits<LANES, NV, BF16, VEC>(a.logits, t * a.ld, masked ? 0 : E, j, x);
         float top = x[0];
 #pragma unroll
         for (int v = 1; v < NV; ++v)
             top = fmaxf(top, x[v]);
         top = group_max<LANES>(top);
-        const float pf = scores<LANES, NV, SIGMOID>(x, top, r);
+        const float norm = scores<LANES, NV, SIGMOID>(x, top, r);
 #pragma unroll
         for (int v = 0; v < NV; ++v)
-            psum[v] += r[v] * pf;
+            psum[v] += SIGMOID ? r[v] * norm : r[v];
         if (j == 0 && top != kNegInf)
             atomicAdd(&cnt_valid, 1);
         // lane k keeps choice k
@@ -225,83 +270,120 @@ __global__ __launch_bounds__(kGateThreads) void gate_kernel(GateLaunch a)
                 m = fmaxf(m, x[v]);
             m = group_max<LANES>(m);
             int id = 0x7FFFFFFF;
-            float rv = 0.0f;
 #pragma unroll
             for (int v = NV - 1; v >= 0; --v)
-                if (x[v] == m) {
+                if (x[v] == m)
                     id = expert_of<LANES>(v, j);
-                    rv = r[v];
-                }
             const int best = group_min<LANES>(id);
             if (m == kNegInf || best >= E)      // no expert is left (or NaN)
                 break;
-            const bool mine = best == id;
-            rv = group_sum<LANES>(mine ? rv : 0.0f);
+            // the same operations as in scores(): the same value
+            const float rv = SIGMOID ? score<true>(m, top) : score<false>(m, top) * norm;
             total += rv;
             if (j == k) {
                 my_id = best;
                 my_r = rv;
             }
-            if (mine) {
+            if (best == id)
                 atomicAdd(&cnt[best], 1);
 #pragma unroll
-                for (int v = 0; v < NV; ++v)
-                    if (expert_of<LANES>(v, j) == best)
-                        x[v] = kNegInf;
-            }
+            for (int v = 0; v < NV; ++v)
+                if (expert_of<LANES>(v, j) == best)
+                    x[v] = kNegInf;
         }
         if (j < K) {
             float w = my_r;
             if (a.normalize)
                 w = total == 0.0f ? 0.0f : my_r / total;
-            a.topk_idx[(int64_t)t * K + j] = my_id;
-            a.topk_weights[(int64_t)t * K + j] = w * a.scale;
+            a.topk_idx[t * K + j] = my_id;
+            a.topk_weights[t * K + j] = w * a.scale;
         }
     }
+    // over the wave's groups, then over the waves
 #pragma unroll
-    for (int v = 0; v < NV; ++v)
-        sum_p[grp * (LANES * NV) + expert_of<LANES>(v, j)] = psum[v];
+    for (int v = 0; v < NV; ++v) {
+        float p = psum[v];
+        if (LANES <= 16)
+            p += __shfl_xor(p, 16);
+        if (LANES <= 32)
+            p += __shfl_xor(p, 32);
+        if (tid % kWave < LANES)
+            sum_p[tid / kWave * kE + expert_of<LANES>(v, j)] = p;
+    }
     __syncthreads();
-    for (int e = tid; e < E; e += kGateThreads) {
+    const int ld = four(E);
+    if (gridDim.x == 1) {
+        for (int e = tid; e < E; e += threads) {
+            float p = 0.0f;
+            for (int w = 0; w < waves; ++w)
+                p += sum_p[w * kE + e];
+            sum_p[e] = p;               // (row 0: only this thread reads it before)
+        }
+        __syncthreads();
+        gate_loss(a, sum_p, cnt, 1, kE, cnt_valid);
+        return;
+    }
+    for (int e = tid; e < ld; e += threads) {
         float p = 0.0f;
-        for (int g = 0; g < kGroups; ++g)
-            p += sum_p[g * (LANES * NV) + e];
-        a.part_p[(size_t)blockIdx.x * E + e] = p;
-        a.part_n[(size_t)blockIdx.x * (E + 1) + e] = cnt[e];
+        for (int w = 0; w < waves; ++w)
+            p += sum_p[w * kE + e];
+        a.part_p[(size_t)blockIdx.x * ld + e] = p;
+        a.part_n[(size_t)blockIdx.x * ld + e] = cnt[e];
     }
     if (tid == 0)
-        a.part_n[(size_t)blockIdx.x * (E + 1) + E] = cnt_valid;
+        a.part_v[blockIdx.x] = cnt_valid;
 }
 
-int gate_blocks(int T, int E)
+// Launch shape.  A token's rounds are a chain of about 800 instructions, so tokens
+// are spread over the SIMDs before any SIMD gets a second wave to fill its waits:
+// 128 tokens, 256 experts, top-8 take 9.5 + 3.7 us in 32 workgroups of one wave and
+// the second launch, 24.4 in one workgroup of 16 waves; 16384 tokens 15.7 + 7.2 in
+// 256 of 16 waves and 34.2 + 8.9 in 256 of four.  16 tokens (of 16 lanes) go
+// in one workgroup without a second launch.
+struct GateShape {
+    int threads, blocks;
+};
+
+static GateShape gate_shape(int T, int E)
 {
-    const int tokens = kGateThreads / (E <= 256 ? 16 : E <= 512 ? 32 : 64);
-    const int64_t need = ((int64_t)T + tokens - 1) / tokens;
-    return (int)(need < 1 ? 1 : need > kGateMaxBlocks ? kGateMaxBlocks : need);
+    const int lanes = E <= 256 ? 16 : E <= 512 ? 32 : 64;
+    const int64_t waves = ((int64_t)T * lanes + kWave - 1) / kWave;
+    if (waves <= 4)
+        return GateShape{256, 1};
+    const int threads = waves <= kGateMaxBlocks ? 64 : waves <= 4 * kGateMaxBlocks ? 256 : kGateThreads;
+    const int64_t need = (waves * kWave + threads - 1) / threads;
+    return GateShape{threads, (int)(need > kGateMaxBlocks ? kGateMaxBlocks : need)};
+}
+
+size_t gate_workspace(int T, int E)
+{
+    return (size_t)gate_shape(T, E).blocks * (2 * four(E) + 1) * 4;
 }
 
 template <int LANES, int NV, bool BF16, bool VEC>
-static void gate_run(const GateLaunch& L, int blocks, hipStream_t stream)
+static void gate_run(const GateLaunch& L, const GateShape& g, hipStream_t stream)
 {
+    const size_t lds = (size_t)(g.threads / kWave) * LANES * NV * 4;
+    debug_launch("gate", dim3(g.blocks), dim3(g.threads), lds);
     if (L.sigmoid)
-        gate_kernel<LANES, NV, BF16, VEC, true><<<blocks, kGateThreads, 0, stream>>>(L);
+        gate_kernel<LANES, NV, BF16, VEC, true><<<g.blocks, g.threads, lds, stream>>>(L);
     else
-        gate_kernel<LANES, NV, BF16, VEC, false><<<blocks, kGateThreads, 0, stream>>>(L);
+        gate_kernel<LANES, NV, BF16, VEC, false><<<g.blocks, g.threads, lds, stream>>>(L);
 }
 
 template <bool BF16, bool VEC>
-static void gate_pick(const GateLaunch& L, int blocks, hipStream_t stream)
+static void gate_pick(const GateLaunch& L, const GateShape& g, hipStream_t stream)
 {
     if (L.E <= 64)
-        gate_run<16, 4, BF16, VEC>(L, blocks, stream);
+        gate_run<16, 4, BF16, VEC>(L, g, stream);
     else if (L.E <= 128)
-        gate_run<16, 8, BF16, VEC>(L, blocks, stream);
+        gate_run<16, 8, BF16, VEC>(L, g, stream);
     else if (L.E <= 256)
-        gate_run<16, 16, BF16, VEC>(L, blocks, stream);
+        gate_run<16, 16, BF16, VEC>(L, g, stream);
     else if (L.E <= 512)
-        gate_run<32, 16, BF16, VEC>(L, blocks, stream);
+        gate_run<32, 16, BF16, VEC>(L, g, stream);
     else
-        gate_run<64, 16, BF16, VEC>(L, blocks, stream);
+        gate_run<64, 16, BF16, VEC>(L, g, stream);
 }
 
 static bool whole_fours(const void* p, bool bf16, int64_t ld, int E)
@@ -309,22 +391,25 @@ static bool whole_fours(const void* p, bool bf16, int64_t ld, int E)
     return E % 4 == 0 && ld % 4 == 0 && reinterpret_cast<uintptr_t>(p) % (bf16 ? 8 : 16) == 0;
 }
 
-hipError_t launch_gate(const GateLaunch& L, hipStream_t stream)
+hipError_t launch_gate(GateLaunch L, void* ws, hipStream_t stream)
 {
-    const int blocks = gate_blocks(L.T, L.E);
-    debug_launch("gate", dim3(blocks), dim3(kGateThreads), 0);
+    const GateShape g = gate_shape(L.T, L.E);
+    L.part_p = static_cast<float*>(ws);
+    L.part_n = reinterpret_cast<int32_t*>(L.part_p + (size_t)g.blocks * four(L.E));
+    L.part_v = L.part_n + (size_t)g.blocks * four(L.E);
     const bool vec = whole_fours(L.logits, L.bf16, L.ld, L.E);
     if (L.bf16)
-        vec ? gate_pick<true, true>(L, blocks, stream) : gate_pick<true, false>(L, blocks, stream);
+        vec ? gate_pick<true, true>(L, g, stream) : gate_pick<true, false>(L, g, stream);
     else
-        vec ? gate_pick<false, true>(L, blocks, stream) : gate_pick<false, false>(L, blocks, stream);
+        vec ? gate_pick<false, true>(L, g, stream) : gate_pick<false, false>(L, g, stream);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess)
         return e;
-    const int stripes = 1024 / L.E < 1 ? 1 : 1024 / L.E;
-    const size_t lds = (size_t)stripes * L.E * 8;
-    debug_launch("gate_finish", dim3(1), dim3(1024), lds);
-    gate_finish_kernel<<<1, 1024, lds, stream>>>(L, blocks);
+    if (g.blocks == 1)
+        return e;
+    const size_t lds = (size_t)finish_stripes(L.E) * four(L.E) * 8;
+    debug_launch("gate_finish", dim3(1), dim3(kGateThreads), lds);
+    gate_finish_kernel<<<1, kGateThreads, lds, stream>>>(L, g.blocks);
     return hipGetLastError();
 }
 
@@ -337,11 +422,16 @@ hipError_t launch_gate(const GateLaunch& L, hipStream_t stream)
 // d/dr_k, otherwise g_k.  dl = r (dr - <r, dr>) for softmax, r (1 - r) dr for sigmoid.
 // ---------------------------------------------------------------------------
 template <int LANES, int NV, bool BF16, bool VEC, bool SIGMOID>
-__global__ __launch_bounds__(kGateThreads) void gate_backward_kernel(GateBackwardLaunch a)
+__global__ __launch_bounds__(kBackThreads) void gate_backward_kernel(GateBackwardLaunch a)
 {
-    constexpr int kGroups = kGateThreads / LANES;
+    constexpr int kGroups = kBackThreads / LANES;
+    constexpr int kE = LANES * NV;
+    // a token's scores, for the lanes that hold a choice; gradients of the chosen ones
+    __shared__ __align__(16) float lds_r[kGroups][kE], lds_g[kGroups][kE];
     const int tid = threadIdx.x, j = tid % LANES, grp = tid / LANES;
     const int E = a.E, K = a.K;
+    for (int i = j; i < kE; i += LANES)
+        lds_g[grp][i] = 0.0f;
     float d[NV];
     {
         const float V = (float)*a.num_valid;
@@ -352,26 +442,26 @@ __global__ __launch_bounds__(kGateThreads) void gate_backward_kernel(GateBackwar
             d[v] = e < E ? c * (float)a.counts[e] : 0.0f;
         }
     }
-    for (int t = blockIdx.x * kGroups + grp; t < a.T; t += gridDim.x * kGroups) {
+    for (int64_t t = (int64_t)blockIdx.x * kGroups + grp; t < a.T; t += (int64_t)gridDim.x * kGroups) {
         const bool masked = a.token_mask && a.token_mask[t] == 0;
         float x[NV], r[NV], o[NV];
-        load_logits<LANES, NV, BF16, VEC>(a.logits, (int64_t)t * a.ld, masked ? 0 : E, j, x);
+        load_logits<LANES, NV, BF16, VEC>(a.logits, t * a.ld, masked ? 0 : E, j, x);
         float top = x[0];
 #pragma unroll
         for (int v = 1; v < NV; ++v)
             top = fmaxf(top, x[v]);
         top = group_max<LANES>(top);
-        const float pf = scores<LANES, NV, SIGMOID>(x, top, r);
+        const float norm = scores<LANES, NV, SIGMOID>(x, top, r);
         // d loss / d r, from the balance loss
         float dot = 0.0f;
 #pragma unroll
         for (int v = 0; v < NV; ++v)
             dot += r[v] * d[v];
         if (SIGMOID) {
-            dot = group_sum<LANES>(dot) * pf;
+            dot = group_sum<LANES>(dot) * norm;
 #pragma unroll
             for (int v = 0; v < NV; ++v)
-                o[v] = (d[v] - dot) * pf;
+                o[v] = (d[v] - dot) * norm;
         } else {
 #pragma unroll
             for (int v = 0; v < NV; ++v)
@@ -382,36 +472,36 @@ __global__ __launch_bounds__(kGateThreads) void gate_backward_kernel(GateBackwar
             int id = -1;
             float g = 0.0f;
             if (j < K) {
-                const int64_t i = a.topk_idx[(int64_t)t * K + j];
+                const int64_t i = a.topk_idx[t * K + j];
                 id = i >= 0 && i < E ? (int)i : -1;
-                g = id >= 0 ? a.grad_weights[(int64_t)t * K + j] * a.scale : 0.0f;
+                g = id >= 0 ? a.grad_weights[t * K + j] * a.scale : 0.0f;
             }
-            float total = 0.0f, gw = 0.0f;
             if (a.normalize) {
-                // scores of the chosen experts, by the lanes that hold them
-                for (int k = 0; k < K; ++k) {
-                    const int ik = __shfl(id, k, LANES);
-                    const float gk = __shfl(g, k, LANES);
 #pragma unroll
-                    for (int v = 0; v < NV; ++v)
-                        if (expert_of<LANES>(v, j) == ik) {
-                            total += r[v];
-                            gw += gk * r[v];
-                        }
-                }
-                total = group_sum<LANES>(total);
-                gw = group_sum<LANES>(gw);
+                for (int v = 0; v < NV; v += 4)
+                    *reinterpret_cast<float4*>(&lds_r[grp][expert_of<LANES>(v, j)]) = float4{r[v], r[v + 1], r[v + 2], r[v + 3]};
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+                const float rk = id >= 0 ? lds_r[grp][id] : 0.0f;
+                const float total = group_sum<LANES>(rk), gw = group_sum<LANES>(g * rk);
                 const float inv = total == 0.0f ? 0.0f : 1.0f / total;
-                g = id >= 0 ? (g - gw * inv) * inv : 0.0f;
+                g = (g - gw * inv) * inv;
             }
-            for (int k = 0; k < K; ++k) {
-                const int ik = __shfl(id, k, LANES);
-                const float gk = __shfl(g, k, LANES);
+            // to the lanes that hold the chosen experts, and back to zeros for the next token
+            if (id >= 0)
+                atomicAdd(&lds_g[grp][id], g);
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
-                for (int v = 0; v < NV; ++v)
-                    if (expert_of<LANES>(v, j) == ik)
-                        o[v] += gk;
+            for (int v = 0; v < NV; v += 4) {
+                const float4 q = *reinterpret_cast<const float4*>(&lds_g[grp][expert_of<LANES>(v, j)]);
+                o[v] += q.x;
+                o[v + 1] += q.y;
+                o[v + 2] += q.z;
+                o[v + 3] += q.w;
             }
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            if (id >= 0)
+                lds_g[grp][id] = 0.0f;
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         }
         if (SIGMOID) {
 #pragma unroll
@@ -430,7 +520,7 @@ __global__ __launch_bounds__(kGateThreads) void gate_backward_kernel(GateBackwar
 #pragma unroll
         for (int v = 0; v < NV; v += 4) {
             const int e = expert_of<LANES>(v, j);
-            const int64_t at = (int64_t)t * E + e;
+            const int64_t at = t * E + e;
             if (VEC) {
                 if (e < E) {
                     if (BF16) {
@@ -459,13 +549,13 @@ __global__ __launch_bounds__(kGateThreads) void gate_backward_kernel(GateBackwar
 template <int LANES, int NV, bool BF16, bool VEC>
 static void gate_backward_run(const GateBackwardLaunch& L, hipStream_t stream)
 {
-    const int64_t need = ((int64_t)L.T + kGateThreads / LANES - 1) / (kGateThreads / LANES);
+    const int64_t need = ((int64_t)L.T + kBackThreads / LANES - 1) / (kBackThreads / LANES);
     const int blocks = (int)(need > 2048 ? 2048 : need);
-    debug_launch("gate_backward", dim3(blocks), dim3(kGateThreads), 0);
+    debug_launch("gate_backward", dim3(blocks), dim3(kBackThreads), 0);
     if (L.sigmoid)
-        gate_backward_kernel<LANES, NV, BF16, VEC, true><<<blocks, kGateThreads, 0, stream>>>(L);
+        gate_backward_kernel<LANES, NV, BF16, VEC, true><<<blocks, kBackThreads, 0, stream>>>(L);
     else
-        gate_backward_kernel<LANES, NV, BF16, VEC, false><<<blocks, kGateThreads, 0, stream>>>(L);
+        gate_backward_kernel<LANES, NV, BF16, VEC, false><<<blocks, kBackThreads, 0, stream>>>(L);
 }
 
 template <bool BF16, bool VEC>

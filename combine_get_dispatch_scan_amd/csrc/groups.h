@@ -45,37 +45,34 @@ __device__ __forceinline__ bool row_in_group(const Groups& g, int r)
 }
 
 // Running count of the groups' row tiles of TILE rows: prefix[i] = tiles of groups
-// before i (LDS, num + 1 entries); WHICH: all, only the full ones, or only the
-// groups' last, partly filled ones.  The first wave fills it; the caller
-// synchronises.
-enum { kAllTiles, kFullTiles, kPartTiles };
-
-template <int TILE, int WHICH = kAllTiles>
+// before i (LDS, num + 1 entries).  The first wave fills it; the caller
+// synchronises.  Groups that do not overlap have at most rows / TILE + num tiles;
+// offsets that make them overlap are cut off at 2^30.
+template <int TILE>
 __device__ __forceinline__ void tile_prefix(const Groups& g, int* prefix)
 {
     if (threadIdx.x >= kWave)
         return;
     const int lane = threadIdx.x;
-    int run = 0;
+    int64_t run = 0;
     if (lane == 0)
         prefix[0] = 0;
     for (int base = 0; base < g.num; base += kWave) {
-        int n = 0;
+        int64_t n = 0;
         if (base + lane < g.num) {
             int b, e;
             group_bounds(g, base + lane, b, e);
-            const int full = (e - b) / TILE, part = (e - b) % TILE != 0;
-            n = WHICH == kAllTiles ? full + part : WHICH == kFullTiles ? full : part;
+            n = ((int64_t)e - b + TILE - 1) / TILE;
         }
 #pragma unroll
         for (int d = 1; d < kWave; d <<= 1) {
-            const int o = __shfl_up(n, d);
+            const int64_t o = __shfl_up((long long)n, d);
             if (lane >= d)
                 n += o;
         }
         if (base + lane < g.num)
-            prefix[base + lane + 1] = run + n;
-        run += readlane(n, kWave - 1);
+            prefix[base + lane + 1] = (int)(run + n < (1 << 30) ? run + n : 1 << 30);
+        run += __shfl((long long)n, kWave - 1);
     }
 }
 
