@@ -174,12 +174,31 @@ __device__ __forceinline__ void copy_scales(const TileSource& t, int kb, int KB,
     }
 }
 
-__device__ __forceinline__ i32x8 read_fragment(const uint8_t* lds, int row, int lane)
+// The permutation of row r's chunks, w's and x's: the eight rows that lanes read
+// together (see read_w, read_x) have eight different ones.
+__device__ __forceinline__ int place_w(int r) { return (r & 3) | ((r >> 1) & 4); }
+__device__ __forceinline__ int place_x(int r) { return r & 7; }
+
+__device__ __forceinline__ i32x8 read_fragment(const uint8_t* row, int place, int lane)
 {
-    const int c = lane >> 4, sw = row & 7;
-    const u32x4 lo = *reinterpret_cast<const u32x4*>(lds + row * kQBlock + ((c ^ sw) << 4));
-    const u32x4 hi = *reinterpret_cast<const u32x4*>(lds + row * kQBlock + (((c + 4) ^ sw) << 4));
+    const int c = lane >> 4;
+    const u32x4 lo = *reinterpret_cast<const u32x4*>(row + ((c ^ place) << 4));
+    const u32x4 hi = *reinterpret_cast<const u32x4*>(row + (((c + 4) ^ place) << 4));
     return join(lo, hi);
+}
+
+__device__ __forceinline__ i32x8 read_x(const uint8_t* lds, int row0, int r, int lane)
+{
+    const int row = row0 + 16 * r + (lane & 15);
+    return read_fragment(lds + row * kQBlock, place_x(row), lane);
+}
+
+// Column tiles 2i and 2i + 1 take every other four of 32 columns, so that a lane's
+// results of both are eight neighbouring columns (one 16-byte store).
+__device__ __forceinline__ i32x8 read_w(const uint8_t* lds, int col0, int c, int lane)
+{
+    const int row = col0 + 32 * (c >> 1) + ((lane & 12) << 1) + (lane & 3) + 4 * (c & 1);
+    return read_fragment(lds + row * kQBlock, place_w(row), lane);
 }
 
 // One K block: the wave's 4 row tiles x 8 column tiles.  A matrix instruction's
@@ -190,18 +209,18 @@ __device__ __forceinline__ void compute_stage(const uint8_t* lx, const uint8_t* 
 {
     i32x8 x[4], w[3];
     f32x4 d[4];
-    w[0] = read_fragment(lw, col0 + (lane & 15), lane);
+    w[0] = read_w(lw, col0, 0, lane);
 #pragma unroll
     for (int r = 0; r < 4; ++r)
-        x[r] = read_fragment(lx, row0 + 16 * r + (lane & 15), lane);
-    w[1] = read_fragment(lw, col0 + 16 + (lane & 15), lane);
+        x[r] = read_x(lx, row0, r, lane);
+    w[1] = read_w(lw, col0, 1, lane);
 #pragma unroll
     for (int i = 0; i < 32 + 3; ++i) {
         const int c = i >> 2, r = i & 3;
         if (i < 32)
             d[r] = mfma_fp8(w[c % 3], x[r]);
         if (r == 0 && c + 2 < 8)
-            w[(c + 2) % 3] = read_fragment(lw, col0 + 16 * (c + 2) + (lane & 15), lane);
+            w[(c + 2) % 3] = read_w(lw, col0, c + 2, lane);
         if (i >= 3) {
             const int pc = (i - 3) >> 2, pr = (i - 3) & 3;
 #pragma unroll
@@ -238,12 +257,11 @@ __global__ __launch_bounds__(512, 2) void gemm_tile_kernel(GemmLaunch a)
         src.w = a.w + ((size_t)g * N + n0) * K;
         src.xs = a.x_scales + scale_at(m0, 0, KB, a.x_scale_ld);
         const int last_row = end - 1 - m0, last_col = N - 1 - n0;   // rows past the end: the last one again
-        const int chunk = ((lane & 7) ^ (lane >> 3)) * 16;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int r = (8 * i + wave) * 8 + (lane >> 3);
-            src.xo[i] = (uint32_t)min(r, last_row) * K + chunk;
-            src.wo[i] = (uint32_t)min(r, last_col) * K + chunk;
+            src.xo[i] = (uint32_t)min(r, last_row) * K + ((lane & 7) ^ place_x(r)) * 16;
+            src.wo[i] = (uint32_t)min(r, last_col) * K + ((lane & 7) ^ place_w(r)) * 16;
         }
         {
             const int r = min((wave & 3) * 64 + lane, last_row);
@@ -301,11 +319,13 @@ __global__ __launch_bounds__(512, 2) void gemm_tile_kernel(GemmLaunch a)
                 const int row = row0 + 16 * r + (lane & 15);
                 if (row > last_row)
                     continue;
-                uint16_t* o = a.out + (size_t)(m0 + row) * N + n0 + col0 + 4 * (lane >> 4);
+                uint16_t* o = a.out + (size_t)(m0 + row) * N + n0 + col0 + 8 * (lane >> 4);
 #pragma unroll
-                for (int c = 0; c < 8; ++c)
-                    *reinterpret_cast<uint2*>(o + 16 * c) =
-                        uint2{pack2_bf16(acc[r][c][0], acc[r][c][1]), pack2_bf16(acc[r][c][2], acc[r][c][3])};
+                for (int c = 0; c < 8; c += 2)
+                    store16_hint<false>(o + 16 * c, u32x4{pack2_bf16(acc[r][c][0], acc[r][c][1]),
+                                                          pack2_bf16(acc[r][c][2], acc[r][c][3]),
+                                                          pack2_bf16(acc[r][c + 1][0], acc[r][c + 1][1]),
+                                                          pack2_bf16(acc[r][c + 1][2], acc[r][c + 1][3])});
             }
         }
         // the last barrier lies behind every read of lsw and the stages: the next tile may overwrite them
