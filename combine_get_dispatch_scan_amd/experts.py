@@ -134,11 +134,11 @@ def _on(t, *others):
 
 def _stream(t):
     import torch
-    return ctypes.c_void_p(torch.cuda.current_stream(t.device).cuda_stream)
+    return torch._C._cuda_getCurrentRawStream(t.device.index)
 
 
 def _shape(t, want, name):
-    if tuple(t.shape) != tuple(want):
+    if t.shape != want:
         raise ValueError(f"{name} must have shape {list(want)}, got {list(t.shape)}")
 
 
@@ -247,17 +247,21 @@ def gate(logits, num_topk: int, *, score: str = "softmax", normalize: bool = Tru
             token_mask = token_mask.view(torch.uint8)
     dev = logits.device
     with _on(logits, token_mask, ws):
+        K = max(int(num_topk), 0)
+        idx = torch.empty((T, K), dtype=torch.int64, device=dev)
+        w = torch.empty((T, K), dtype=torch.float32, device=dev)
+        # the workspace and the small outputs, in one allocation
+        n = 0 if ws is not None else (ep_gate_workspace_bytes(T, E) + 3) // 4
+        own, counts, valid, loss = torch.empty(n + E + 2, dtype=torch.int32, device=dev).split((n, E, 1, 1))
+        loss = loss.view(torch.float32)
         if ws is None:
-            ws = torch.empty(max(1, ep_gate_workspace_bytes(T, E)), dtype=torch.uint8, device=dev)
-        K = int(num_topk)
-        idx = torch.empty((T, max(K, 0)), dtype=torch.int64, device=dev)
-        w = torch.empty((T, max(K, 0)), dtype=torch.float32, device=dev)
-        counts = torch.empty(E, dtype=torch.int32, device=dev)
-        valid = torch.empty(1, dtype=torch.int32, device=dev)
-        loss = torch.empty(1, dtype=torch.float32, device=dev)
+            at, nbytes = own.data_ptr(), 4 * n
+        else:
+            at, nbytes = _ptr(ws, "u8", "ws"), ws.numel()
+        p = counts.data_ptr()
         _check(ep_gate(logits.data_ptr(), bf16, ld, T, E, K, _SCORES[score], bool(normalize), scale,
-                       balance_coef, _ptr(token_mask, "u8", "token_mask"), _ptr(idx), _ptr(w), _ptr(counts),
-                       _ptr(valid), _ptr(loss), _ptr(ws, "u8", "ws"), ws.numel(), _stream(logits)))
+                       balance_coef, _ptr(token_mask, "u8", "token_mask"), idx.data_ptr(), w.data_ptr(), p,
+                       p + 4 * E, p + 4 * E + 4, at, nbytes, _stream(logits)))
     return Gate(idx, w, counts, valid, loss, _SCORES[score], bool(normalize), float(scale),
                 float(balance_coef), token_mask)
 
