@@ -123,7 +123,7 @@ __global__ __launch_bounds__(256) void gemm_skinny_kernel(GemmLaunch a)
 // which global chunk lands where), so that eight rows read at the same chunk
 // hit all banks once.
 //
-// 65536 rows in 32 groups, N = 4096, K = 7168: 1865 us, 2.07 PFLOP/s, where a library
+// 65536 rows in 32 groups, N = 4096, K = 7168: 1836-1876 us, 2.05-2.10 PFLOP/s, where a library
 // product of E4M3 matrices with one scale reaches 2.9 (8192^3) to 3.2 (16384^3).  The
 // matrix cores are busy for half of the time.  Taken apart: the copies alone
 // take 1320-1400 us (two stages in flight; 1830 us with one, as here, when nothing is

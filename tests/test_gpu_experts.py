@@ -401,6 +401,16 @@ def test_weight_gradient_layouts(ep):
     _check_wgrad(ep, [2, 0, 1] * 200, 128, 128, torch.bfloat16)
 
 
+@pytest.mark.parametrize("N,K", [(128, 128), (384, 640), (512, 256)])
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+def test_weight_gradient_many_rows(ep, N, K, dtype):
+    """The larger tile, which many rows a group choose."""
+    dt = getattr(torch, dtype)
+    _check_wgrad(ep, [1030, 0, 700], N, K, dt)
+    _check_wgrad(ep, [1100, 3], N, K, dt, column_major=True)
+    _check_wgrad(ep, [600, 5], N, K, dt, stride=600)
+
+
 # ----------------------------------------------------------------------------
 # SwiGLU
 # ----------------------------------------------------------------------------
