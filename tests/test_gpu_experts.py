@@ -119,6 +119,8 @@ def _check_gate(ep, x, K, score, normalize, mask=None, scale=1.5, coef=0.02, see
     (1, 1, 1, "float32"), (3, 7, 7, "float32"), (16, 256, 8, "bfloat16"), (17, 60, 4, "float32"),
     (65, 64, 16, "bfloat16"), (129, 128, 6, "float32"), (300, 256, 8, "float32"), (5000, 100, 3, "bfloat16"),
     (40, 384, 6, "bfloat16"), (21, 1024, 16, "float32"), (700, 1000, 2, "bfloat16"),
+    # workgroups of 16 waves at each way of holding a token, and of four waves
+    (2100, 1024, 8, "float32"), (4200, 512, 6, "bfloat16"), (1500, 64, 2, "float32"), (17000, 60, 4, "float32"),
 ])
 def test_gate(ep, score, normalize, T, E, K, dtype):
     x = (2 * _randn(_gen(T + E), T, E)).to(getattr(torch, dtype))
