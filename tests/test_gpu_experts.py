@@ -736,3 +736,42 @@ def test_binding_refusals_on_the_gpu(ep):
     assert not ep.grouped_wgrad_fp8(torch.empty(0, 128, dtype=torch.bfloat16, device=dev), e, es, off).any()
     assert ep.quantize_rows(torch.empty(0, 256, dtype=torch.bfloat16, device=dev))[0].shape == (0, 256)
     assert ep.swiglu_fp8(torch.empty(0, 256, dtype=torch.bfloat16, device=dev), checkpoint=True)[2].shape == (0, 256)
+
+
+def test_late_first_group_and_byte_codes(ep):
+    """Groups that begin behind the first row and end before the last; codes passed as uint8."""
+    dev = _dev()
+    g = _gen(31)
+    x, xs, _ = _fp8_rows(g, 200, 384)
+    w, ws = (_randn(g, 3, 256, 384) * 50).to(F8), torch.rand(3, 2, 3, generator=g, device=dev) + 0.1
+    off = torch.tensor([20, 20, 150, 190], dtype=torch.int32, device=dev)
+    for expected in (1, 10, 50, 1000000):
+        out = torch.full((200, 256), 5.0, dtype=torch.bfloat16, device=dev)
+        ep.grouped_gemm_fp8(x.view(torch.uint8), xs, w.view(torch.uint8), ws, off, expected_rows=expected, out=out)
+        assert (out[:20] == 5).all() and (out[190:] == 5).all() and (out[20:190] != 5).any(1).all()
+    dw = ep.grouped_wgrad_fp8(_randn(g, 200, 256).bfloat16(), x, xs, off)
+    assert not dw[0].any() and dw[1].any() and dw[2].any()
+
+
+def test_reused_gate_workspace(ep):
+    x = _randn(_gen(32), 500, 64)
+    ws = torch.empty(ep.ep_gate_workspace_bytes(500, 64), dtype=torch.uint8, device=x.device)
+    a, b, c = (ep.gate(x, 4, balance_coef=1.0, ws=t) for t in (ws, ws, None))
+    assert torch.equal(a.loss, b.loss) and torch.equal(a.loss, c.loss) and torch.equal(a.topk_weights, c.topk_weights)
+
+
+def test_autograd_without_tokens_and_under_capture(ep):
+    import combine_get_dispatch_scan_amd.autograd as A
+    dev = _dev()
+    x = torch.zeros(0, 256, device=dev, dtype=torch.bfloat16, requires_grad=True)
+    logits = torch.zeros(0, 8, device=dev, requires_grad=True)
+    w1, w2 = (torch.randn(8, 256, n, device=dev, requires_grad=True) for n in (256, 128))
+    g = A.gate(logits, 2, balance_coef=1.0)
+    (A.experts(x, g.topk_idx, g.topk_weights, w1, w2).float().sum() + g.loss.sum()).backward()
+    assert not w1.grad.any() and not w2.grad.any() and x.grad.shape == (0, 256)
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with pytest.raises(RuntimeError, match="cannot be captured"):
+        with torch.cuda.graph(graph):
+            A.gate(w1.detach()[0].requires_grad_(), 2)
+    torch.cuda.synchronize()
