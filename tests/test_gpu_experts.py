@@ -775,3 +775,16 @@ def test_autograd_without_tokens_and_under_capture(ep):
         with torch.cuda.graph(graph):
             A.gate(w1.detach()[0].requires_grad_(), 2)
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_gate_nan_logit_is_not_chosen_and_shows_in_the_loss(ep, score):
+    x = _randn(_gen(33), 40, 100)
+    x[7, 5] = math.nan
+    x[9] = math.nan
+    q = ep.gate(x, 8, score=score, balance_coef=1.0)
+    ids = q.topk_idx.cpu()
+    assert ((ids >= -1) & (ids < 100)).all() and 5 not in ids[7] and (ids[9] == -1).all()
+    assert math.isnan(float(q.loss))
+    keep = [i for i in range(40) if i not in (7, 9)]
+    assert torch.equal(q.topk_idx[keep], ep.gate(x[keep].contiguous(), 8, score=score).topk_idx)
