@@ -250,18 +250,16 @@ def gate(logits, num_topk: int, *, score: str = "softmax", normalize: bool = Tru
         K = max(int(num_topk), 0)
         idx = torch.empty((T, K), dtype=torch.int64, device=dev)
         w = torch.empty((T, K), dtype=torch.float32, device=dev)
-        # the workspace and the small outputs, in one allocation
-        n = 0 if ws is not None else (ep_gate_workspace_bytes(T, E) + 3) // 4
-        own, counts, valid, loss = torch.empty(n + E + 2, dtype=torch.int32, device=dev).split((n, E, 1, 1))
-        loss = loss.view(torch.float32)
+        # storage of their own: a kept loss holds no workspace, and torch counts changes of each by itself
+        counts = torch.empty(E, dtype=torch.int32, device=dev)
+        valid = torch.empty(1, dtype=torch.int32, device=dev)
+        loss = torch.empty(1, dtype=torch.float32, device=dev)
         if ws is None:
-            at, nbytes = own.data_ptr(), 4 * n
-        else:
-            at, nbytes = _ptr(ws, "u8", "ws"), ws.numel()
-        p = counts.data_ptr()
+            ws = torch.empty(ep_gate_workspace_bytes(T, E), dtype=torch.uint8, device=dev)
         _check(ep_gate(logits.data_ptr(), bf16, ld, T, E, K, _SCORES[score], bool(normalize), scale,
-                       balance_coef, _ptr(token_mask, "u8", "token_mask"), idx.data_ptr(), w.data_ptr(), p,
-                       p + 4 * E, p + 4 * E + 4, at, nbytes, _stream(logits)))
+                       balance_coef, _ptr(token_mask, "u8", "token_mask"), idx.data_ptr(), w.data_ptr(),
+                       counts.data_ptr(), valid.data_ptr(), loss.data_ptr(), _ptr(ws, "u8", "ws"), ws.numel(),
+                       _stream(logits)))
     return Gate(idx, w, counts, valid, loss, _SCORES[score], bool(normalize), float(scale),
                 float(balance_coef), token_mask)
 
