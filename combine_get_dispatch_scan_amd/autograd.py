@@ -43,7 +43,7 @@ from . import dispatch_backward as _dispatch_backward
 from . import gate as _gate_call
 from . import gate_backward as _gate_backward
 from . import get_dispatch_layout as _get_dispatch_layout
-from . import (grouped_gemm_fp8, grouped_wgrad_fp8, quantize_rows, quantize_weights, swiglu_fp8,
+from . import (Gate, grouped_gemm_fp8, grouped_wgrad_fp8, quantize_rows, quantize_weights, swiglu_fp8,
                swiglu_fp8_backward)
 
 
@@ -126,24 +126,28 @@ def _eager_only(what):
 
 
 class _Gate(torch.autograd.Function):
+    # ctx holds no output but through save_for_backward: a node that holds its own
+    # outputs, which hold the node, is never freed
     @staticmethod
     def forward(ctx, logits, num_topk, options, out):
         g = _gate_call(logits.detach(), num_topk, **options)
         out.append(g)
-        ctx.g = g
-        ctx.save_for_backward(logits)
+        ctx.save_for_backward(logits, g.topk_idx, g.num_tokens_per_expert)
+        ctx.num_valid, ctx.token_mask = g.num_valid, g.token_mask
+        ctx.options = g.score, g.normalize, g.scale, g.balance_coef
         ctx.mark_non_differentiable(g.topk_idx, g.num_tokens_per_expert)
         ctx.set_materialize_grads(False)
         return g.topk_weights, g.loss, g.topk_idx, g.num_tokens_per_expert
 
     @staticmethod
     def backward(ctx, grad_weights, grad_loss, *_):
-        logits, = ctx.saved_tensors
+        logits, idx, counts = ctx.saved_tensors
         if grad_weights is not None:
             grad_weights = grad_weights.contiguous()
         if grad_loss is not None:
             grad_loss = grad_loss.contiguous()
-        return _gate_backward(logits.detach(), ctx.g, grad_weights, grad_loss), None, None, None
+        g = Gate(idx, None, counts, ctx.num_valid, None, *ctx.options, ctx.token_mask)
+        return _gate_backward(logits.detach(), g, grad_weights, grad_loss), None, None, None
 
 
 def gate(logits, num_topk: int, **options):
