@@ -132,8 +132,7 @@ class _Gate(torch.autograd.Function):
     def forward(ctx, logits, num_topk, options, out):
         g = _gate_call(logits.detach(), num_topk, **options)
         out.append(g)
-        ctx.save_for_backward(logits, g.topk_idx, g.num_tokens_per_expert)
-        ctx.num_valid, ctx.token_mask = g.num_valid, g.token_mask
+        ctx.save_for_backward(logits, g.topk_idx, g.num_tokens_per_expert, g.num_valid, g.token_mask)
         ctx.options = g.score, g.normalize, g.scale, g.balance_coef
         ctx.mark_non_differentiable(g.topk_idx, g.num_tokens_per_expert)
         ctx.set_materialize_grads(False)
@@ -141,18 +140,19 @@ class _Gate(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, grad_weights, grad_loss, *_):
-        logits, idx, counts = ctx.saved_tensors
+        logits, idx, counts, valid, mask = ctx.saved_tensors
         if grad_weights is not None:
             grad_weights = grad_weights.contiguous()
         if grad_loss is not None:
             grad_loss = grad_loss.contiguous()
-        g = Gate(idx, None, counts, ctx.num_valid, None, *ctx.options, ctx.token_mask)
+        g = Gate(idx, None, counts, valid, None, *ctx.options, mask)
         return _gate_backward(logits.detach(), g, grad_weights, grad_loss), None, None, None
 
 
 def gate(logits, num_topk: int, **options):
     """The gate (same options) with gradients of its weights and its balance loss
-    towards the logits."""
+    towards the logits.  Backward reads the logits, ids, counts, num_valid and
+    token_mask again: changing one of them in place before is an error."""
     _eager_only("gate")
     kept = []
     w, loss, _, _ = _Gate.apply(logits, num_topk, options, kept)

@@ -104,3 +104,16 @@ def test_gate_refuses_changed_ids_and_counts(autograd):
     logits.grad = None
     (3.0 * autograd.gate(logits, 2, balance_coef=0.1).loss.sum()).backward()
     assert torch.equal(once, logits.grad) and once.any()
+
+
+@pytest.mark.parametrize("dtype", [torch.bool, torch.uint8])
+def test_gate_refuses_changed_mask_and_token_count(autograd, dtype):
+    for change in (lambda g, mask: mask.fill_(1), lambda g, mask: g.num_valid.fill_(6)):
+        logits, mask = torch.randn(6, 8, requires_grad=True), torch.tensor([1, 1, 0, 1, 0, 1]).to(dtype)
+        g = autograd.gate(logits, 2, balance_coef=0.1, token_mask=mask)
+        change(g, mask)
+        with pytest.raises(RuntimeError, match="inplace"):
+            g.loss.sum().backward()
+    logits, mask = torch.randn(6, 8, requires_grad=True), torch.tensor([1, 1, 0, 1, 0, 1]).to(dtype)
+    autograd.gate(logits, 2, balance_coef=0.1, token_mask=mask).loss.sum().backward()
+    assert logits.grad[0].any() and not logits.grad[2].any() and not logits.grad[4].any()
