@@ -28,11 +28,12 @@ Only argument marshalling happens here; every step runs in the HIP kernels.
 These functions are for eager autograd: a backward pass captured into a graph
 while an eager graph of the same leaves is alive ends the process in torch, so
 ``gate`` and ``experts`` refuse to be captured (the plain calls they are made of
-can be).
+can be).  None of them has a second derivative: asking for one raises.
 """
 from __future__ import annotations
 
 import dataclasses
+import functools
 
 import torch
 
@@ -45,6 +46,41 @@ from . import gate_backward as _gate_backward
 from . import get_dispatch_layout as _get_dispatch_layout
 from . import (Gate, grouped_gemm_fp8, grouped_wgrad_fp8, quantize_rows, quantize_weights, swiglu_fp8,
                swiglu_fp8_backward)
+
+
+class _NoSecondDerivative(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, anchor, what, *grads):
+        ctx.what = what
+        ctx.set_materialize_grads(False)
+        return grads
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise RuntimeError(f"{ctx.what} has no second derivative")
+
+
+def _first_order(backward):
+    """Marks a backward pass that cannot be differentiated itself.  Under create_graph
+    its gradients may be used, but differentiating through them raises, also where the
+    incoming gradient is a constant: they depend on the forward pass's inputs."""
+    what = backward.__qualname__
+
+    @functools.wraps(backward)
+    def run(ctx, *grads):
+        with torch.no_grad():
+            out = backward(ctx, *grads)
+        if not torch.is_grad_enabled():
+            return out
+        out = out if isinstance(out, tuple) else (out,)
+        at = [i for i, g in enumerate(out) if g is not None]
+        marked = _NoSecondDerivative.apply(torch.empty(0, requires_grad=True), what, *(out[i] for i in at))
+        out = list(out)
+        for i, g in zip(at, marked):
+            out[i] = g
+        return tuple(out)
+
+    return run
 
 
 class _Routing:
@@ -65,6 +101,7 @@ class _Dispatch(torch.autograd.Function):
         return recv
 
     @staticmethod
+    @_first_order
     def backward(ctx, grad_recv):
         return _dispatch_backward(grad_recv.contiguous(), ctx.handle), None, None, None
 
@@ -94,6 +131,7 @@ class _Combine(torch.autograd.Function):
         return out
 
     @staticmethod
+    @_first_order
     def backward(ctx, grad_out):
         y, w = ctx.saved_tensors
         want_w = w is not None and ctx.needs_input_grad[1]
@@ -139,6 +177,7 @@ class _Gate(torch.autograd.Function):
         return g.topk_weights, g.loss, g.topk_idx, g.num_tokens_per_expert
 
     @staticmethod
+    @_first_order
     def backward(ctx, grad_weights, grad_loss, *_):
         logits, idx, counts, valid, mask = ctx.saved_tensors
         if grad_weights is not None:
@@ -176,6 +215,7 @@ class _Experts(torch.autograd.Function):
         return _combine(y2, h)
 
     @staticmethod
+    @_first_order
     def backward(ctx, grad_out):
         x8, xs, a8, a_s, c8, cs, y2, w1t, s1t, w2t, s2t = ctx.saved_tensors
         h = ctx.handle

@@ -65,6 +65,73 @@ def _stand_in_gate_backward(logits, g, grad_weights=None, grad_loss=None):
     return x.grad * grad_loss
 
 
+class _Handle:
+    """Of a dense layout whose pair count the host has not read."""
+    num_recv = None
+
+    class c:
+        static_cap, expert_alignment = 0, 1
+
+
+def _stand_in_layer(monkeypatch, A):
+    """Dispatch, products, SwiGLU and combine as calls on CPU tensors that only keep the
+    shapes (values are copies of the inputs); returns the list of what was called, with
+    what was asked of it."""
+    log = []
+
+    def wide(x, n):
+        return x[:, :1].float().expand(-1, n).contiguous()
+
+    def scales(x):
+        return torch.ones(len(x), x.shape[1] // 128)
+
+    def dispatch(x, w, layout, fp8, *a):
+        log.append(("dispatch", None))
+        x = x.repeat_interleave(2, 0)
+        return x, scales(x) if fp8 else None, _Handle()
+
+    def weights(w, transposed=False):
+        log.append(("weights", transposed))
+        t = w.transpose(1, 2).contiguous()
+        return ep.Fp8Weights(w, w[:, ::128, ::128], *((t, t[:, ::128, ::128]) if transposed else (None, None)))
+
+    def product(x, xs, w, ws, h):
+        y = wide(x, w.shape[1])
+        log.append(("product", weakref.ref(y)))
+        return y
+
+    def swiglu(h, handle, checkpoint=False):
+        log.append(("swiglu", checkpoint))
+        a = wide(h, h.shape[1] // 2)
+        return (a, scales(a)) + ((wide(h, h.shape[1]), scales(h)) if checkpoint else (None, None))
+
+    def combine(y, h, w=None):
+        return wide(y[::2], y.shape[1])
+
+    def combine_backward(go, h, y=None, topk_weights=None, grad_y=None):
+        log.append(("combine_backward", y is not None))
+        return go.repeat_interleave(2, 0), None if y is None else torch.ones(len(go), 2)
+
+    def wgrad(dy, x, xs, h, out_dtype=None):
+        log.append(("wgrad", out_dtype))
+        return torch.ones(4, dy.shape[1], x.shape[1], dtype=out_dtype)
+
+    def swiglu_backward(da, ck, cs, h, quantize=True):
+        log.append(("swiglu_backward", quantize))
+        return (wide(da, ck.shape[1]),) + ((wide(da, ck.shape[1]), cs) if quantize else (None, None))
+
+    class Layout:
+        handle = _Handle()
+
+    for name, f in (("_get_dispatch_layout", lambda *a: Layout()), ("_dispatch", dispatch),
+                    ("quantize_weights", weights), ("grouped_gemm_fp8", product), ("swiglu_fp8", swiglu),
+                    ("_combine", combine), ("_combine_backward", combine_backward), ("grouped_wgrad_fp8", wgrad),
+                    ("quantize_rows", lambda x, h: (x, scales(x))), ("swiglu_fp8_backward", swiglu_backward),
+                    ("_dispatch_backward", lambda g, h: wide(g[::2], g.shape[1]))):
+        monkeypatch.setattr(A, name, f)
+    return log
+
+
 @pytest.fixture
 def autograd(monkeypatch):
     import combine_get_dispatch_scan_amd.autograd as A
@@ -117,3 +184,29 @@ def test_gate_refuses_changed_mask_and_token_count(autograd, dtype):
     logits, mask = torch.randn(6, 8, requires_grad=True), torch.tensor([1, 1, 0, 1, 0, 1]).to(dtype)
     autograd.gate(logits, 2, balance_coef=0.1, token_mask=mask).loss.sum().backward()
     assert logits.grad[0].any() and not logits.grad[2].any() and not logits.grad[4].any()
+
+
+def test_second_derivatives_are_refused(autograd, monkeypatch):
+    """The backward passes are kernels without a derivative of their own: differentiating
+    through them raises instead of dropping terms."""
+    logits = torch.randn(6, 8, requires_grad=True)
+    plain, = torch.autograd.grad(autograd.gate(logits, 2, balance_coef=0.1).loss.sum(), logits)
+    first, = torch.autograd.grad(autograd.gate(logits, 2, balance_coef=0.1).loss.sum(), logits, create_graph=True)
+    assert torch.equal(plain, first) and not plain.requires_grad
+    with pytest.raises(RuntimeError, match="no second derivative"):
+        first.square().sum().backward()
+    _stand_in_layer(monkeypatch, autograd)
+    x, w = torch.randn(6, 128, requires_grad=True), torch.rand(6, 2, requires_grad=True)
+    w1, w2 = torch.randn(4, 256, 128), torch.randn(4, 128, 128)
+    out = autograd.experts(x, torch.zeros(6, 2, dtype=torch.int64), w, w1, w2)
+    first, = torch.autograd.grad(out.square().sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError, match="no second derivative"):
+        first.square().sum().backward()
+    recv, handle = autograd.dispatch(x, torch.zeros(6, 2, dtype=torch.int64), w, 4, 1)
+    first, = torch.autograd.grad(recv.square().sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError, match="no second derivative"):
+        first.square().sum().backward()
+    y = torch.randn(12, 128, requires_grad=True)
+    first, = torch.autograd.grad(autograd.combine(y, handle, w).square().sum(), y, create_graph=True)
+    with pytest.raises(RuntimeError, match="no second derivative"):
+        first.square().sum().backward()
