@@ -200,9 +200,9 @@ def gate(logits, num_topk: int, **options):
 
 class _Experts(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, topk_weights, w1, w2, layout):
+    def forward(ctx, x, topk_weights, w1, w2, layout, grad_enabled):
         x8, xs, h = _dispatch(x.detach().contiguous(), topk_weights.detach().contiguous(), layout, True)
-        train = any(ctx.needs_input_grad)
+        train = grad_enabled and any(ctx.needs_input_grad)      # (inputs that need one count under no_grad too)
         q1 = quantize_weights(w1.detach().contiguous(), transposed=train)
         q2 = quantize_weights(w2.detach().contiguous(), transposed=train)
         y1 = grouped_gemm_fp8(x8, xs, q1.codes, q1.scales, h)
@@ -219,7 +219,7 @@ class _Experts(torch.autograd.Function):
     def backward(ctx, grad_out):
         x8, xs, a8, a_s, c8, cs, y2, w1t, s1t, w2t, s2t = ctx.saved_tensors
         h = ctx.handle
-        want_x, want_w, want_1, want_2, _ = ctx.needs_input_grad
+        want_x, want_w, want_1, want_2 = ctx.needs_input_grad[:4]
         gy, gw = _combine_backward(grad_out.contiguous(), h, y=y2 if want_w else None)   # dispatch's copy of the weights
         gx = g1 = g2 = None
         if want_2:
@@ -232,7 +232,7 @@ class _Experts(torch.autograd.Function):
                 g1 = grouped_wgrad_fp8(gh, x8, xs, h, out_dtype=ctx.dtypes[0])
             if want_x:
                 gx = _dispatch_backward(grouped_gemm_fp8(gh8, ghs, w1t, s1t, h), h)
-        return gx, (gw if want_w else None), g1, g2, None
+        return gx, (gw if want_w else None), g1, g2, None, None
 
 
 def experts(x, topk_idx, topk_weights, w1, w2, num_partitions: int = 1):
@@ -246,4 +246,6 @@ def experts(x, topk_idx, topk_weights, w1, w2, num_partitions: int = 1):
             w1.shape[2] != x.shape[1] or w2.shape[1] != x.shape[1]:
         raise ValueError(f"x [T, H], w1 [E, 2 * I, H] and w2 [E, H, I] do not fit: {list(x.shape)}, "
                          f"{list(w1.shape)}, {list(w2.shape)}")
-    return _Experts.apply(x, topk_weights, w1, w2, _get_dispatch_layout(topk_idx, E, num_partitions))
+    layout = _get_dispatch_layout(topk_idx, E, num_partitions)
+    # inside forward gradients are always off
+    return _Experts.apply(x, topk_weights, w1, w2, layout, torch.is_grad_enabled())

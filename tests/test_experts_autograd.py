@@ -210,3 +210,27 @@ def test_second_derivatives_are_refused(autograd, monkeypatch):
     first, = torch.autograd.grad(autograd.combine(y, handle, w).square().sum(), y, create_graph=True)
     with pytest.raises(RuntimeError, match="no second derivative"):
         first.square().sum().backward()
+
+
+def _layer_inputs(dtype=torch.float32):
+    return (torch.randn(6, 128), torch.zeros(6, 2, dtype=torch.int64), torch.rand(6, 2),
+            torch.randn(4, 256, 128), torch.randn(4, 128, 128))
+
+
+def test_experts_without_gradients_does_no_training_work(autograd, monkeypatch):
+    """Inference with parameters writes no transposed weights and no checkpoint."""
+    log = _stand_in_layer(monkeypatch, autograd)
+    x, idx, w, w1, w2 = _layer_inputs()
+    w1, w2 = torch.nn.Parameter(w1), torch.nn.Parameter(w2)
+    for mode in (torch.no_grad, torch.inference_mode):
+        log.clear()
+        with mode():
+            out = autograd.experts(x, idx, w, w1, w2)
+        assert not out.requires_grad
+        assert [v for k, v in log if k == "weights"] == [False, False]
+        assert [v for k, v in log if k == "swiglu"] == [False]
+    log.clear()
+    out = autograd.experts(x, idx, w, w1, w2)
+    assert [v for k, v in log if k == "swiglu"] == [True] and out.requires_grad
+    out.sum().backward()
+    assert w1.grad is not None and w2.grad is not None
