@@ -19,10 +19,13 @@ requires grad).  Receive rows that no pair maps to get a zero gradient.
     (task_loss(out) + g.loss).backward()
 
 ``experts`` is dispatch, the two FP8 products with SwiGLU between them, and
-combine.  It keeps its activations for the backward pass in 8 bits (the
-dispatched rows, SwiGLU's input and output), and its gradient rows are
+combine.  It keeps what the wanted gradients read: activations in 8 bits (the
+dispatched rows, SwiGLU's input and output), and, only where topk_weights needs
+a gradient, the second product's output in bf16.  Its gradient rows are
 quantised the same way for the products towards the inputs; the quantisers are
-taken as straight-through.
+taken as straight-through.  The weights are quantised in every call: inference
+with constant weights keeps ``quantize_weights``'s result and makes the plain
+calls.
 
 Only argument marshalling happens here; every step runs in the HIP kernels.
 These functions are for eager autograd: a backward pass captured into a graph
@@ -201,17 +204,19 @@ def gate(logits, num_topk: int, **options):
 class _Experts(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, topk_weights, w1, w2, layout, grad_enabled):
+        # inputs that need a gradient count under no_grad too; `inner`: the gradient passes SwiGLU
+        want_x, want_w, want_1, want_2 = (grad_enabled and n for n in ctx.needs_input_grad[:4])
+        inner = want_x or want_1
         x8, xs, h = _dispatch(x.detach().contiguous(), topk_weights.detach().contiguous(), layout, True)
-        train = grad_enabled and any(ctx.needs_input_grad)      # (inputs that need one count under no_grad too)
-        q1 = quantize_weights(w1.detach().contiguous(), transposed=train)
-        q2 = quantize_weights(w2.detach().contiguous(), transposed=train)
+        q1 = quantize_weights(w1.detach().contiguous(), transposed=want_x)
+        q2 = quantize_weights(w2.detach().contiguous(), transposed=inner)
         y1 = grouped_gemm_fp8(x8, xs, q1.codes, q1.scales, h)
-        a8, a_s, c8, cs = swiglu_fp8(y1, h, checkpoint=train)
+        a8, a_s, c8, cs = swiglu_fp8(y1, h, checkpoint=inner)
         y2 = grouped_gemm_fp8(a8, a_s, q2.codes, q2.scales, h)
-        if train:
-            ctx.handle = h
-            ctx.dtypes = w1.dtype, w2.dtype
-            ctx.save_for_backward(x8, xs, a8, a_s, c8, cs, y2, q1.codes_t, q1.scales_t, q2.codes_t, q2.scales_t)
+        ctx.handle = h
+        ctx.dtypes = w1.dtype, w2.dtype
+        ctx.save_for_backward(*((x8, xs) if want_1 else (None, None)), *((a8, a_s) if want_2 else (None, None)),
+                              c8, cs, y2 if want_w else None, q1.codes_t, q1.scales_t, q2.codes_t, q2.scales_t)
         return _combine(y2, h)
 
     @staticmethod
@@ -220,7 +225,7 @@ class _Experts(torch.autograd.Function):
         x8, xs, a8, a_s, c8, cs, y2, w1t, s1t, w2t, s2t = ctx.saved_tensors
         h = ctx.handle
         want_x, want_w, want_1, want_2 = ctx.needs_input_grad[:4]
-        gy, gw = _combine_backward(grad_out.contiguous(), h, y=y2 if want_w else None)   # dispatch's copy of the weights
+        gy, gw = _combine_backward(grad_out.contiguous(), h, y=y2 if want_w else None)     # dispatch's copy of the weights
         gx = g1 = g2 = None
         if want_2:
             g2 = grouped_wgrad_fp8(gy, a8, a_s, h, out_dtype=ctx.dtypes[1])

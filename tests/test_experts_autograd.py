@@ -234,3 +234,28 @@ def test_experts_without_gradients_does_no_training_work(autograd, monkeypatch):
     assert [v for k, v in log if k == "swiglu"] == [True] and out.requires_grad
     out.sum().backward()
     assert w1.grad is not None and w2.grad is not None
+
+
+@pytest.mark.parametrize("need", [(a, b, c, d) for a in (0, 1) for b in (0, 1) for c in (0, 1) for d in (0, 1)
+                                  if a or b or c or d])
+def test_experts_keeps_what_backward_reads(autograd, monkeypatch, need):
+    """The second product's bf16 output is kept only for the gradient of the gate's weights,
+    and each 8-bit tensor only where a gradient reads it."""
+    log = _stand_in_layer(monkeypatch, autograd)
+    x, idx, w, w1, w2 = _layer_inputs()
+    for t, n in zip((x, w, w1, w2), need):
+        t.requires_grad_(bool(n))
+    want_x, want_w, want_1, want_2 = map(bool, need)
+    out = autograd.experts(x, idx, w, w1, w2)
+    products = [v for k, v in log if k == "product"]
+    gc.collect()
+    assert products[0]() is None and (products[1]() is not None) == want_w
+    assert [v for k, v in log if k == "weights"] == [want_x, want_x or want_1]
+    assert [v for k, v in log if k == "swiglu"] == [want_x or want_1]
+    saved = out.grad_fn.saved_tensors
+    assert sum(t is not None for t in saved) == 2 * (want_1 + want_2 + (want_x or want_1)) + want_w + \
+        2 * (want_x + (want_x or want_1))
+    out.sum().backward()
+    assert [t.grad is not None for t in (x, w, w1, w2)] == [want_x, want_w, want_1, want_2]
+    assert [v for k, v in log if k == "combine_backward"] == [want_w]
+    assert sum(k == "wgrad" for k, _ in log) == want_1 + want_2
