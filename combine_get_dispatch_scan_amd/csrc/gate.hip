@@ -115,21 +115,34 @@ __device__ __forceinline__ void load_logits(const void* logits, int64_t at, int 
     }
 }
 
+// What a token's scores are taken relative to, so that the largest is at least 1/2:
+// softmax e^top, sigmoid e^min(top, 0).  A sigmoid is 0 in fp32 below -103, but the
+// ratios of such scores, which is what weights and probabilities are, are not.
 template <bool SIGMOID>
-__device__ __forceinline__ float score(float x, float top)
+__device__ __forceinline__ float base_of(float top)
 {
-    return SIGMOID ? 1.0f / (1.0f + expf(-x)) : expf(x - top);
+    return SIGMOID ? fminf(top, 0.0f) : top;
 }
 
-// Scores r of the token's experts (softmax: times `norm`) and norm, 1 / their sum.
-// A token without any expert left (every logit -inf) has r = 0 and norm = 0.
+template <bool SIGMOID>
+__device__ __forceinline__ float score(float x, float base)
+{
+    if (!SIGMOID)
+        return expf(x - base);
+    const float e = expf(-fabsf(x));
+    return (x > 0.0f ? 1.0f : base == 0.0f ? e : expf(x - base)) / (1.0f + e);
+}
+
+// Scores r of the token's experts over e^base (softmax: times `norm`) and norm, 1 /
+// their sum.  A token without any expert left (every logit -inf) has r = 0 and norm = 0.
 template <int LANES, int NV, bool SIGMOID>
 __device__ __forceinline__ float scores(const float (&x)[NV], float top, float (&r)[NV])
 {
+    const float base = base_of<SIGMOID>(top);
     float sum = 0.0f;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-        r[v] = !SIGMOID && top == kNegInf ? 0.0f : score<SIGMOID>(x[v], top);
+        r[v] = top == kNegInf ? 0.0f : score<SIGMOID>(x[v], base);
         sum += r[v];
     }
     sum = group_sum<LANES>(sum);
@@ -254,6 +267,7 @@ __global__ __launch_bounds__(kGateThreads) void gate_kernel(GateLaunch a)
         for (int v = 1; v < NV; ++v)
             top = fmaxf(top, x[v]);
         top = group_max<LANES>(top);
+        const float base = base_of<SIGMOID>(top);
         const float norm = scores<LANES, NV, SIGMOID>(x, top, r);
 #pragma unroll
         for (int v = 0; v < NV; ++v)
@@ -278,7 +292,7 @@ __global__ __launch_bounds__(kGateThreads) void gate_kernel(GateLaunch a)
             if (m == kNegInf || best >= E)      // no expert is left (or NaN)
                 break;
             // the same operations as in scores(): the same value
-            const float rv = SIGMOID ? score<true>(m, top) : score<false>(m, top) * norm;
+            const float rv = SIGMOID ? score<true>(m, base) : score<false>(m, base) * norm;
             total += rv;
             if (j == k) {
                 my_id = best;
@@ -292,7 +306,7 @@ __global__ __launch_bounds__(kGateThreads) void gate_kernel(GateLaunch a)
                     x[v] = kNegInf;
         }
         if (j < K) {
-            float w = my_r;
+            float w = SIGMOID ? my_r * expf(base) : my_r;
             if (a.normalize)
                 w = total == 0.0f ? 0.0f : my_r / total;
             a.topk_idx[t * K + j] = my_id;
@@ -419,7 +433,8 @@ hipError_t launch_gate(GateLaunch L, void* ws, hipStream_t stream)
 //   softmax  dl = p (d - <p, d>) + ...             sigmoid  ds = (d - <p, d>) / sum r + ...
 // and for the chosen experts, with g = scale * grad_weights and wn = r / sum of
 // the chosen r:  normalised  (g_k - <g, wn>) / sum of the chosen r  is added to
-// d/dr_k, otherwise g_k.  dl = r (dr - <r, dr>) for softmax, r (1 - r) dr for sigmoid.
+// d/dr_k, otherwise g_k.  dl = r (dr - <r, dr>) for softmax, r (1 - r) dr for sigmoid,
+// where r dr is the same with r and its sums over e^base.
 // ---------------------------------------------------------------------------
 template <int LANES, int NV, bool BF16, bool VEC, bool SIGMOID>
 __global__ __launch_bounds__(kBackThreads) void gate_backward_kernel(GateBackwardLaunch a)
@@ -452,6 +467,7 @@ __global__ __launch_bounds__(kBackThreads) void gate_backward_kernel(GateBackwar
             top = fmaxf(top, x[v]);
         top = group_max<LANES>(top);
         const float norm = scores<LANES, NV, SIGMOID>(x, top, r);
+        const float lift = SIGMOID && top != kNegInf ? expf(base_of<SIGMOID>(top)) : 1.0f;   // e^base
         // d loss / d r, from the balance loss
         float dot = 0.0f;
 #pragma unroll
@@ -485,6 +501,8 @@ __global__ __launch_bounds__(kBackThreads) void gate_backward_kernel(GateBackwar
                 const float total = group_sum<LANES>(rk), gw = group_sum<LANES>(g * rk);
                 const float inv = total == 0.0f ? 0.0f : 1.0f / total;
                 g = (g - gw * inv) * inv;
+            } else if (SIGMOID) {
+                g *= lift;
             }
             // to the lanes that hold the chosen experts, and back to zeros for the next token
             if (id >= 0)
@@ -506,7 +524,7 @@ __global__ __launch_bounds__(kBackThreads) void gate_backward_kernel(GateBackwar
         if (SIGMOID) {
 #pragma unroll
             for (int v = 0; v < NV; ++v)
-                o[v] = r[v] * (1.0f - r[v]) * o[v];
+                o[v] = r[v] * (1.0f - r[v] * lift) * o[v];
         } else {
             dot = 0.0f;
 #pragma unroll

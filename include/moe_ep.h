@@ -511,7 +511,9 @@ int ep_e4m3fn_encode(const float* in, uint8_t* out, int64_t n, hipStream_t strea
  *   choice    the K largest logits, ties to the lower id, in descending order.
  *             A logit of -inf is never chosen; a token with fewer than K others
  *             gets id -1 and weight 0 in the places left (dispatch skips them)
- *   weights   scale * r_k / (sum of the chosen r) if normalize, else scale * r_k
+ *   weights   scale * r_k / (sum of the chosen r) if normalize, else scale * r_k.
+ *             Ratios of sigmoid scores hold also where the scores are below
+ *             fp32's range (logits under -88); scale * r_k itself is then 0
  *   loss      balance_coef * sum_e f_e * P_e, f_e = E*n_e / (K*V),
  *             P_e = (sum over the V tokens that count of p_te) / V; 0 when V = 0
  * A token counts unless token_mask is 0 for it or all its logits are -inf; a

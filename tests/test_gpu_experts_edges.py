@@ -1,0 +1,85 @@
+"""GPU checks of the expert layer where its formulas are hard to hold: sigmoid
+scores far from zero.  Tolerances count roundings as in test_gpu_experts.py."""
+import numpy as np
+import pytest
+
+from test_gpu_experts import U, _dev, _gen, _randn
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+
+# ----------------------------------------------------------------------------
+# sigmoid scores far from zero
+# ----------------------------------------------------------------------------
+
+def _sigmoid_gate64(x, idx, normalize, scale, coef, gw, gl):
+    """Weights, loss, gradient and its terms' magnitudes, for the choice idx, from
+    log s = -log(1 + e^-x) in 64 bits: no score underflows or cancels.  With q = s / max s,
+        w = q_k / sum of the chosen q  (or s_k),    p = q / sum q,
+        dl = (1 - s) (p (d - <p, d>) + wn (g - <g, wn>))      (normalised; else s g)"""
+    T, E = x.shape
+    K = idx.shape[1]
+    ls = -np.logaddexp(0.0, -x)
+    s, rest = np.exp(ls), np.exp(-np.logaddexp(0.0, x))        # s and 1 - s
+    q = np.exp(ls - ls.max(1, keepdims=True))
+    p = q / q.sum(1, keepdims=True)
+    sel = np.zeros((T, E), bool)
+    np.put_along_axis(sel, idx, True, 1)
+    part = np.where(sel, ls, -np.inf)
+    wn = np.where(sel, np.exp(part - part.max(1, keepdims=True)), 0.0)
+    wn = wn / wn.sum(1, keepdims=True) if normalize else np.where(sel, s, 0.0)
+    n = sel.sum(0)
+    f = E * n / (K * T)
+    loss = coef * (f * p.sum(0)).sum() / T
+    g = np.zeros((T, E))
+    np.put_along_axis(g, idx, gw * scale, 1)
+    d = (coef * gl * f / T)[None, :]
+    back = (g * wn).sum(1, keepdims=True) if normalize else 0.0
+    mag = (np.abs(g) * wn).sum(1, keepdims=True) if normalize else 0.0
+    dl = rest * (p * (d - (p * d).sum(1, keepdims=True)) + wn * (g - back))
+    mg = rest * (p * (np.abs(d) + (p * np.abs(d)).sum(1, keepdims=True)) + wn * (np.abs(g) + mag))
+    return np.take_along_axis(wn, idx, 1) * scale, loss, dl, mg
+
+
+def _far_logits(where, T, E, dtype):
+    u = torch.rand(T, E, generator=_gen(T + E), device=_dev())
+    x = {"low": -80 - 40 * u, "vanishing": -104 + 17 * u, "lowest": torch.full_like(u, torch.finfo(dtype).min),
+         "saturated": 12 + 18 * u, "both": torch.where(u < 0.5, -100 + 60 * u, 20 + 30 * u)}[where]
+    return x.to(dtype)
+
+
+def _check_far(ep, where, E, K, dtype, normalize):
+    T, scale, coef = 37, 1.5, 0.5
+    x = _far_logits(where, T, E, dtype)
+    g = _gen(3)
+    gw, gl = _randn(g, T, K), torch.ones(1, device=x.device)
+    q = ep.gate(x, K, score="sigmoid", normalize=normalize, scale=scale, balance_coef=coef)
+    got = ep.gate_backward(x, q, gw, gl)
+    x64 = x.double().cpu().numpy()
+    w, loss, dl, mag = _sigmoid_gate64(x64, q.topk_idx.cpu().numpy(), normalize, scale, coef,
+                                       gw.double().cpu().numpy(), 1.0)
+    # a score: the logit's distance from the largest (one rounding, times the exponent's size), the
+    # exponential and the quotient (2 u each), the sum of E positive terms (at most 16 + 6 in a chain)
+    rel = (2 * (x64.max(1) - x64.min(1)).max() + 40) * U
+    # fp32's normal numbers end at 1.2e-38: factors of at most 100 beside them
+    tiny = 1e-36
+    assert (np.abs(q.topk_weights.double().cpu().numpy() - w) <= 2 * rel * w + tiny).all()
+    if normalize:
+        assert (np.abs(q.topk_weights.double().sum(1).cpu().numpy() - scale) <= 2 * (rel + K * U) * scale).all()
+    assert abs(float(q.loss) - loss) <= (rel + 100 * U) * loss + tiny
+    out = 2.0 ** -8 if dtype == torch.bfloat16 else U
+    assert (np.abs(got.double().cpu().numpy() - dl) <= 4 * rel * mag + out * np.abs(dl) + tiny).all()
+
+
+FAR = [(e, k, d) for e, k in ((8, 3), (64, 4), (300, 8), (1000, 4)) for d in (torch.float32, torch.bfloat16)]
+
+
+@pytest.mark.parametrize("where", ["low", "vanishing", "lowest"])
+@pytest.mark.parametrize("normalize", [True, False])
+@pytest.mark.parametrize("E,K,dtype", FAR)
+def test_sigmoid_gate_at_low_logits(ep, where, normalize, E, K, dtype):
+    """Scores under fp32's smallest number still have ratios: weights sum to the scale, the
+    probabilities of the balance loss to one, and gradients are finite."""
+    _check_far(ep, where, E, K, dtype, normalize)
