@@ -124,25 +124,30 @@ __device__ __forceinline__ float base_of(float top)
     return SIGMOID ? fminf(top, 0.0f) : top;
 }
 
+// A score over e^base, and for sigmoid 1 - s = s(-x) from the same exponential (a
+// subtraction leaves 1% of it wrong at x = 12 and nothing at 17).
 template <bool SIGMOID>
-__device__ __forceinline__ float score(float x, float base)
+__device__ __forceinline__ float score(float x, float base, float& rest)
 {
     if (!SIGMOID)
         return expf(x - base);
     const float e = expf(-fabsf(x));
+    rest = (x > 0.0f ? e : 1.0f) / (1.0f + e);
     return (x > 0.0f ? 1.0f : base == 0.0f ? e : expf(x - base)) / (1.0f + e);
 }
 
-// Scores r of the token's experts over e^base (softmax: times `norm`) and norm, 1 /
-// their sum.  A token without any expert left (every logit -inf) has r = 0 and norm = 0.
+// Scores r of the token's experts over e^base (softmax: times `norm`), for sigmoid their
+// rest 1 - s, and norm, 1 / the sum of r.  A token without any expert left (every logit
+// -inf) has r = rest = norm = 0.
 template <int LANES, int NV, bool SIGMOID>
-__device__ __forceinline__ float scores(const float (&x)[NV], float top, float (&r)[NV])
+__device__ __forceinline__ float scores(const float (&x)[NV], float top, float (&r)[NV], float (&rest)[NV])
 {
     const float base = base_of<SIGMOID>(top);
     float sum = 0.0f;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-        r[v] = top == kNegInf ? 0.0f : score<SIGMOID>(x[v], base);
+        rest[v] = 0.0f;
+        r[v] = top == kNegInf ? 0.0f : score<SIGMOID>(x[v], base, rest[v]);
         sum += r[v];
     }
     sum = group_sum<LANES>(sum);
@@ -259,7 +264,7 @@ __global__ __launch_bounds__(kGateThreads) void gate_kernel(GateLaunch a)
         psum[v] = 0.0f;
     for (int64_t t = (int64_t)blockIdx.x * groups + grp; t < a.T; t += (int64_t)gridDim.x * groups) {
         const bool masked = a.token_mask && a.token_mask[t] == 0;
-        float x[NV], r[NV];
+        float x[NV], r[NV], rest[NV];
         // a masked token's logits are not looked at: they may hold anything
         load_logits<LANES, NV, BF16, VEC>(a.logits, t * a.ld, masked ? 0 : E, j, x);
         float top = x[0];
@@ -268,7 +273,7 @@ __global__ __launch_bounds__(kGateThreads) void gate_kernel(GateLaunch a)
             top = fmaxf(top, x[v]);
         top = group_max<LANES>(top);
         const float base = base_of<SIGMOID>(top);
-        const float norm = scores<LANES, NV, SIGMOID>(x, top, r);
+        const float norm = scores<LANES, NV, SIGMOID>(x, top, r, rest);
 #pragma unroll
         for (int v = 0; v < NV; ++v)
             psum[v] += SIGMOID ? r[v] * norm : r[v];
@@ -292,7 +297,8 @@ __global__ __launch_bounds__(kGateThreads) void gate_kernel(GateLaunch a)
             if (m == kNegInf || best >= E)      // no expert is left (or NaN)
                 break;
             // the same operations as in scores(): the same value
-            const float rv = SIGMOID ? score<true>(m, base) : score<false>(m, base) * norm;
+            float unused;
+            const float rv = SIGMOID ? score<true>(m, base, unused) : score<false>(m, base, unused) * norm;
             total += rv;
             if (j == k) {
                 my_id = best;
@@ -459,15 +465,14 @@ __global__ __launch_bounds__(kBackThreads) void gate_backward_kernel(GateBackwar
     }
     for (int64_t t = (int64_t)blockIdx.x * kGroups + grp; t < a.T; t += (int64_t)gridDim.x * kGroups) {
         const bool masked = a.token_mask && a.token_mask[t] == 0;
-        float x[NV], r[NV], o[NV];
+        float x[NV], r[NV], rest[NV], o[NV];
         load_logits<LANES, NV, BF16, VEC>(a.logits, t * a.ld, masked ? 0 : E, j, x);
         float top = x[0];
 #pragma unroll
         for (int v = 1; v < NV; ++v)
             top = fmaxf(top, x[v]);
         top = group_max<LANES>(top);
-        const float norm = scores<LANES, NV, SIGMOID>(x, top, r);
-        const float lift = SIGMOID && top != kNegInf ? expf(base_of<SIGMOID>(top)) : 1.0f;   // e^base
+        const float norm = scores<LANES, NV, SIGMOID>(x, top, r, rest);
         // d loss / d r, from the balance loss
         float dot = 0.0f;
 #pragma unroll
@@ -502,7 +507,7 @@ __global__ __launch_bounds__(kBackThreads) void gate_backward_kernel(GateBackwar
                 const float inv = total == 0.0f ? 0.0f : 1.0f / total;
                 g = (g - gw * inv) * inv;
             } else if (SIGMOID) {
-                g *= lift;
+                g *= expf(base_of<SIGMOID>(top));      // r is over e^base
             }
             // to the lanes that hold the chosen experts, and back to zeros for the next token
             if (id >= 0)
@@ -524,7 +529,7 @@ __global__ __launch_bounds__(kBackThreads) void gate_backward_kernel(GateBackwar
         if (SIGMOID) {
 #pragma unroll
             for (int v = 0; v < NV; ++v)
-                o[v] = r[v] * (1.0f - r[v] * lift) * o[v];
+                o[v] = r[v] * rest[v] * o[v];
         } else {
             dot = 0.0f;
 #pragma unroll

@@ -83,3 +83,11 @@ def test_sigmoid_gate_at_low_logits(ep, where, normalize, E, K, dtype):
     """Scores under fp32's smallest number still have ratios: weights sum to the scale, the
     probabilities of the balance loss to one, and gradients are finite."""
     _check_far(ep, where, E, K, dtype, normalize)
+
+
+@pytest.mark.parametrize("where", ["saturated", "both"])
+@pytest.mark.parametrize("normalize", [True, False])
+@pytest.mark.parametrize("E,K,dtype", FAR)
+def test_sigmoid_gate_at_saturated_logits(ep, where, normalize, E, K, dtype):
+    """Scores near one: 1 - s is e^-x, not what a subtraction leaves of it."""
+    _check_far(ep, where, E, K, dtype, normalize)
