@@ -524,13 +524,16 @@ def dispatch_backward(grad_recv, handle: Handle, grad_x=None):
 
 def combine_backward(grad_out, handle: Handle, y=None, topk_weights=None, grad_y=None):
     """grad_out: bf16 [T, H].  Returns (grad_y bf16 [capacity, H], grad_w fp32
-    [T, K] or None when y is None).  Rows of grad_y that no pair maps to are
-    left as allocated."""
+    [T, K] or None when y is None).  Rows of grad_y that no pair maps to keep
+    what they held; without grad_y they are zeros in an aligned layout, whose
+    padding rows are rows of their expert to the calls that take grad_y on
+    (the weight gradient sums over them), and else undefined."""
     import torch
     c = handle.c
     dev = grad_out.device
     if grad_y is None:
-        grad_y = torch.empty((c.capacity_rows, c.hidden), dtype=torch.bfloat16, device=dev)
+        new = torch.zeros if c.expert_alignment > 1 else torch.empty
+        grad_y = new((c.capacity_rows, c.hidden), dtype=torch.bfloat16, device=dev)
     grad_w = None if y is None else torch.empty((c.num_tokens, c.num_topk), dtype=torch.float32,
                                                 device=dev)
     _check(ep_combine_backward(_ptr(grad_out, "bf16", "grad_out"), _ptr(y, "bf16", "y"), c,

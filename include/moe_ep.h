@@ -494,7 +494,9 @@ int ep_e4m3fn_encode(const float* in, uint8_t* out, int64_t n, hipStream_t strea
  * capacity_rows.  The offsets are read on the device only (no host sync), and
  * clamped to num_rows there.  Rows of no group are neither read nor written.
  * The padding rows of an aligned layout count as rows of their group (dispatch
- * wrote them as zeros).  Widths are multiples of 128, at most EP_MAX_HIDDEN.
+ * wrote them as zeros; ep_combine_backward leaves those of grad_y alone, so
+ * clear grad_y before it where these calls take it on).
+ * Widths are multiples of 128, at most EP_MAX_HIDDEN.
  * FP8 rows are E4M3FN codes [num_rows][width] with fp32 scales, one per row and
  * 128 channels: scale_ld 0: [num_rows][width/128]; else [width/128][scale_ld],
  * scale_ld >= num_rows and a multiple of 4.  Code and bf16 arrays are 16-byte

@@ -1,9 +1,10 @@
 """GPU checks of the expert layer where its formulas are hard to hold: sigmoid
-scores far from zero.  Tolerances count roundings as in test_gpu_experts.py."""
+scores far from zero, padding rows on the way back.  Tolerances count roundings as
+in test_gpu_experts.py."""
 import numpy as np
 import pytest
 
-from test_gpu_experts import U, _dev, _gen, _randn
+from test_gpu_experts import U, _dev, _gen, _layer_case, _randn
 
 pytestmark = pytest.mark.gpu
 
@@ -91,3 +92,36 @@ def test_sigmoid_gate_at_low_logits(ep, where, normalize, E, K, dtype):
 def test_sigmoid_gate_at_saturated_logits(ep, where, normalize, E, K, dtype):
     """Scores near one: 1 - s is e^-x, not what a subtraction leaves of it."""
     _check_far(ep, where, E, K, dtype, normalize)
+
+
+# ----------------------------------------------------------------------------
+# padding rows of an aligned layout on the way back
+# ----------------------------------------------------------------------------
+
+@pytest.mark.parametrize("alignment", [64, 128])
+def test_weight_gradients_of_an_aligned_layout(ep, alignment):
+    """The rows combine's backward pass writes go into the weight gradient with the padding
+    rows of their blocks: whatever the memory held before, those add nothing."""
+    x, logits, w1, w2 = _layer_case(21)
+    q1, q2 = ep.quantize_weights(w1, True), ep.quantize_weights(w2, True)
+    go = _randn(_gen(22), *x.shape).bfloat16()
+
+    def grads(align):
+        g = ep.gate(logits, 2)
+        lay = ep.get_dispatch_layout(g.topk_idx, 8, 1, expert_alignment=align)
+        x8, xs, h = ep.dispatch(x, g.topk_weights, lay, True)
+        a8, a_s, ck, cs = ep.swiglu_fp8(ep.grouped_gemm_fp8(x8, xs, q1.codes, q1.scales, h), h, checkpoint=True)
+        y = ep.grouped_gemm_fp8(a8, a_s, q2.codes, q2.scales, h)
+        spoilt = torch.full((x8.shape[0], x.shape[1]), float("nan"), dtype=torch.bfloat16, device=x.device)
+        del spoilt                                  # the allocator hands this memory out again
+        gy, gw = ep.combine_backward(go, h, y=y)
+        g8, gs = ep.quantize_rows(gy, h)
+        gh, gh8, ghs = ep.swiglu_fp8_backward(ep.grouped_gemm_fp8(g8, gs, q2.codes_t, q2.scales_t, h), ck, cs, h)
+        gx = ep.dispatch_backward(ep.grouped_gemm_fp8(gh8, ghs, q1.codes_t, q1.scales_t, h), h)
+        f32 = torch.float32
+        return (gx, gw, ep.grouped_wgrad_fp8(gh, x8, xs, h, out_dtype=f32),
+                ep.grouped_wgrad_fp8(gy, a8, a_s, h, out_dtype=f32))
+
+    for a, b in zip(grads(alignment), grads(1)):
+        # the same rows in the same order, zeros behind them
+        assert torch.equal(a, b)
