@@ -355,7 +355,7 @@ hipError_t launch_grouped_gemm(const GemmLaunch& L, hipStream_t stream)
     if (L.groups.rows == 0 || L.groups.num == 0)
         return hipSuccess;
     const int m = L.expected_rows;
-    const int64_t tiles = (int64_t)L.groups.num * ((m + kTile - 1) / kTile) * ((L.N + kTile - 1) / kTile);
+    const int64_t tiles = (int64_t)L.groups.num * (((int64_t)m + kTile - 1) / kTile) * ((L.N + kTile - 1) / kTile);
     if (m <= 8) {
         skinny_run<1, 4>(L, stream);
     } else if (m <= 16) {

@@ -1,6 +1,10 @@
 """GPU checks of the expert layer where its formulas are hard to hold: sigmoid
-scores far from zero, padding rows on the way back.  Tolerances count roundings as
-in test_gpu_experts.py."""
+scores far from zero, padding rows on the way back, choices at the ends of their
+range.  Tolerances count roundings as in test_gpu_experts.py."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 
@@ -125,3 +129,28 @@ def test_weight_gradients_of_an_aligned_layout(ep, alignment):
     for a, b in zip(grads(alignment), grads(1)):
         # the same rows in the same order, zeros behind them
         assert torch.equal(a, b)
+
+
+# ----------------------------------------------------------------------------
+# arguments at the ends of their range
+# ----------------------------------------------------------------------------
+
+def test_expected_rows_at_the_largest_number():
+    """The tile for many rows, also where rows + 255 pass 2^31 (EP_DEBUG is read once per
+    process, so a child process makes the call)."""
+    _dev()
+    code = (
+        "import sys; sys.path.insert(0, %r)\n"
+        "import torch, combine_get_dispatch_scan_amd as ep\n"
+        "d = torch.device('cuda:0')\n"
+        "w = ep.quantize_weights(torch.randn((2, 256, 256), device=d))\n"
+        "x, xs = ep.quantize_rows(torch.randn((64, 256), device=d).bfloat16())\n"
+        "off = torch.tensor([0, 40, 64], dtype=torch.int32, device=d)\n"
+        "for n in (100000, 2**31 - 1):\n"
+        "    ep.grouped_gemm_fp8(x, xs, w.codes, w.scales, off, expected_rows=n)\n"
+        "torch.cuda.synchronize()\n" % os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=100,
+                       env=dict(os.environ, EP_DEBUG="1"))
+    assert r.returncode == 0, r.stderr[-2000:]
+    lines = [l.split()[1] for l in r.stderr.splitlines() if l.startswith("[moe_ep] grouped_gemm")]
+    assert lines == ["grouped_gemm_tile"] * 2
