@@ -142,14 +142,22 @@ def _shape(t, want, name):
         raise ValueError(f"{name} must have shape {list(want)}, got {list(t.shape)}")
 
 
+def _i32(n, name):
+    """n as the int the C call takes it as (ctypes would cut higher bits off)."""
+    if not -2 ** 31 <= n < 2 ** 31:
+        raise ValueError(f"{name}={n} must be less than 2^31")
+    return int(n)
+
+
 def _width(n, name):
-    if n < 128 or n % 128:
+    if _i32(n, name) < 128 or n % 128:
         raise ValueError(f"{name}={n} must be a multiple of 128")
 
 
 def _matrix(t, name):
     if t.dim() != 2:
         raise ValueError(f"{name} must be a matrix [rows, width], got shape {list(t.shape)}")
+    _i32(t.shape[0], "rows")
     return t.shape
 
 
@@ -164,7 +172,7 @@ def _groups(groups, group_stride, like):
         return off, c.num_experts, c.static_cap, max(1, expected)
     if groups.dim() != 1 or groups.numel() < 2:
         raise ValueError(f"groups must be a Handle or row offsets [num_groups + 1], got shape {list(groups.shape)}")
-    return groups, groups.numel() - 1, int(group_stride), 0
+    return groups, _i32(groups.numel() - 1, "num_groups"), group_stride, 0
 
 
 def _group_args(groups, group_stride, like):
@@ -220,6 +228,8 @@ def _logits(logits):
     if logits.dtype not in (torch.float32, torch.bfloat16):
         raise TypeError(f"logits must be torch.float32 or torch.bfloat16, got {logits.dtype}")
     T, E = logits.shape
+    _i32(T, "tokens")
+    _i32(E, "experts")
     if T > 0 and E > 1 and logits.stride(1) != 1:
         raise ValueError("the logits of a token must be contiguous")
     ld = logits.stride(0) if T > 1 else E
@@ -239,6 +249,7 @@ def gate(logits, num_topk: int, *, score: str = "softmax", normalize: bool = Tru
     ep_gate_workspace_bytes(T, E)) may be passed to reuse a workspace."""
     import torch
     T, E, bf16, ld = _logits(logits)
+    K = max(_i32(num_topk, "num_topk"), 0)
     if score not in _SCORES:
         raise ValueError(f"score must be one of {sorted(_SCORES)}, got {score!r}")
     if token_mask is not None:
@@ -247,7 +258,6 @@ def gate(logits, num_topk: int, *, score: str = "softmax", normalize: bool = Tru
             token_mask = token_mask.view(torch.uint8)
     dev = logits.device
     with _on(logits, token_mask, ws):
-        K = max(int(num_topk), 0)
         idx = torch.empty((T, K), dtype=torch.int64, device=dev)
         w = torch.empty((T, K), dtype=torch.float32, device=dev)
         # storage of their own: a kept loss holds no workspace, and torch counts changes of each by itself
@@ -295,6 +305,7 @@ def quantize_rows(x, groups=None, *, group_stride: int = 0, column_major_scales:
     None: every row; else only rows of a group."""
     rows, H = _matrix(x, "x")
     _width(H, "H")
+    group_stride = _i32(group_stride, "group_stride")
     with _on(x):
         args, _ = ((None, 0, 0), 0) if groups is None else _group_args(groups, group_stride, x)
         codes, scales, ld = _new_rows(rows, H, column_major_scales, x.device)
@@ -354,6 +365,7 @@ def grouped_gemm_fp8(x, x_scales, w, w_scales, groups, *, group_stride: int = 0,
     _width(N, "N")
     _shape(w_scales, (G, N // 128, K // 128), "w_scales")
     ld = _row_scales(x_scales, rows, K, column_major_scales, "x_scales")
+    group_stride, expected_rows = _i32(group_stride, "group_stride"), _i32(expected_rows, "expected_rows")
     with _on(x, x_scales, w, w_scales, out):
         args, expected = _group_args(groups, group_stride, x)
         if args[1] != G:
@@ -363,7 +375,7 @@ def grouped_gemm_fp8(x, x_scales, w, w_scales, groups, *, group_stride: int = 0,
         _shape(out, (rows, N), "out")
         _check(ep_grouped_gemm_fp8(_ptr(x, "fp8", "x"), _ptr(x_scales, "f32", "x_scales"), ld,
                                    _ptr(w, "fp8", "w"), _ptr(w_scales, "f32", "w_scales"), *args, rows, N, K,
-                                   int(expected_rows) or expected, _ptr(out, "bf16", "out"), _stream(x)))
+                                   expected_rows or expected, _ptr(out, "bf16", "out"), _stream(x)))
     return out
 
 
@@ -379,6 +391,7 @@ def grouped_wgrad_fp8(grad, x, x_scales, groups, *, group_stride: int = 0, out_d
     _width(K, "K")
     _width(N, "N")
     ld = _row_scales(x_scales, rows, K, column_major_scales, "x_scales")
+    group_stride = _i32(group_stride, "group_stride")
     with _on(x, grad, x_scales, out):
         args, _ = _group_args(groups, group_stride, x)
         if out is None:
@@ -404,6 +417,7 @@ def swiglu_fp8(h, groups=None, *, group_stride: int = 0, checkpoint: bool = Fals
     if W % 2:
         raise ValueError(f"h must be [rows, 2 * inner], got shape {list(h.shape)}")
     _width(inner, "inner")
+    group_stride = _i32(group_stride, "group_stride")
     with _on(h):
         args, _ = ((None, 0, 0), 0) if groups is None else _group_args(groups, group_stride, h)
         codes, scales, ld = _new_rows(rows, inner, column_major_scales, h.device)
@@ -426,6 +440,7 @@ def swiglu_fp8_backward(grad_a, ckpt, ckpt_scales, groups=None, *, group_stride:
     _width(inner, "inner")
     _shape(ckpt, (rows, 2 * inner), "ckpt")
     _shape(ckpt_scales, (rows, 2 * inner // 128), "ckpt_scales")
+    group_stride = _i32(group_stride, "group_stride")
     with _on(grad_a, ckpt, ckpt_scales):
         args, _ = ((None, 0, 0), 0) if groups is None else _group_args(groups, group_stride, grad_a)
         grad_h = torch.empty((rows, 2 * inner), dtype=torch.bfloat16, device=grad_a.device)

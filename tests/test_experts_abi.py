@@ -161,3 +161,33 @@ def test_binding_refuses_cpu_tensors_and_wrong_shapes():
         ep.swiglu_fp8(torch.zeros(3, 200, dtype=torch.bfloat16))
     with pytest.raises(ValueError, match="ckpt"):
         ep.swiglu_fp8_backward(torch.zeros(3, 128, dtype=torch.bfloat16), x, xs)
+
+
+def test_binding_refuses_numbers_past_32_bits():
+    """The C calls take them as int: 2^32 would arrive as 0."""
+    f8 = torch.float8_e4m3fn
+    off = torch.zeros(3, dtype=torch.int32)
+    x, xs = torch.zeros(4, 256, dtype=torch.uint8).view(f8), torch.zeros(4, 2)
+    w, ws = torch.zeros(2, 128, 256, dtype=torch.uint8).view(f8), torch.zeros(2, 1, 2)
+    meta = lambda *s, dt=torch.bfloat16: torch.empty(*s, dtype=dt, device="meta")  # noqa: E731
+    for n in (2 ** 31, 2 ** 32, 2 ** 32 + 5):
+        with pytest.raises(ValueError, match="2\\^31"):
+            ep.gate(meta(n, 1), 1)
+        with pytest.raises(ValueError, match="2\\^31"):
+            ep.gate_backward(meta(n, 1), None)
+        with pytest.raises(ValueError, match="2\\^31"):
+            ep.quantize_rows(meta(n, 128))
+        with pytest.raises(ValueError, match="2\\^31"):
+            ep.swiglu_fp8(meta(n, 256))
+        with pytest.raises(ValueError, match="group_stride"):
+            ep.grouped_gemm_fp8(x, xs, w, ws, off, group_stride=n)
+        with pytest.raises(ValueError, match="group_stride"):
+            ep.quantize_rows(torch.zeros(4, 256, dtype=torch.bfloat16), off, group_stride=n)
+        with pytest.raises(ValueError, match="expected_rows"):
+            ep.grouped_gemm_fp8(x, xs, w, ws, off, expected_rows=n)
+        with pytest.raises(ValueError, match="num_topk"):
+            ep.gate(torch.zeros(4, 8), n)
+        with pytest.raises(ValueError, match="experts"):
+            ep.gate(meta(1, n), 1)
+    with pytest.raises(ValueError, match="2\\^31"):
+        ep.quantize_rows(meta(1, 2 ** 32 + 128))
