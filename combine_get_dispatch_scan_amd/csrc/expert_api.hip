@@ -10,7 +10,8 @@ using moe_ep::hip_fail;
 
 namespace {
 
-constexpr int64_t kMaxUnits = (int64_t)1 << 29;   // 1 x 128 blocks a row launch covers (grid limit)
+// 1 x 128 blocks a row launch covers: 32 a workgroup of 256, and fewer than 2^32 threads.
+constexpr int64_t kMaxUnits = ((int64_t)1 << 29) - 32;
 
 bool width_ok(int w) { return w >= 128 && w <= EP_MAX_HIDDEN && w % 128 == 0; }
 
@@ -57,7 +58,7 @@ int check_units(int rows, int width)
 {
     if ((int64_t)rows * (width / 128) <= kMaxUnits)
         return EP_OK;
-    return fail(EP_EINVAL, "num_rows=%d x width=%d is more than one call covers (2^29 blocks of 128)", rows, width);
+    return fail(EP_EINVAL, "num_rows=%d x width=%d is more than one call covers (2^29 - 32 blocks of 128)", rows, width);
 }
 
 struct GateDims {

@@ -191,3 +191,11 @@ def test_binding_refuses_numbers_past_32_bits():
             ep.gate(meta(1, n), 1)
     with pytest.raises(ValueError, match="2\\^31"):
         ep.quantize_rows(meta(1, 2 ** 32 + 128))
+
+
+@pytest.mark.parametrize("name,args,width", [("ep_quantize_rows", ROWS, "width"), ("ep_swiglu_fp8", SWIGLU, "inner"),
+                                             ("ep_swiglu_fp8_backward", SWIGLU_BACK, "inner")])
+@pytest.mark.parametrize("rows", [1 << 22, (1 << 22) - 1 + (1 << 20)])
+def test_row_calls_refuse_more_than_a_launch_covers(name, args, width, rows):
+    """2^29 blocks of 128 are 2^32 threads, one more than a launch can have."""
+    _refused(getattr(ep, name), args, {width: 16384, "num_rows": rows}, "2^29")
