@@ -49,6 +49,7 @@ from . import gate_backward as _gate_backward
 from . import get_dispatch_layout as _get_dispatch_layout
 from . import (Gate, grouped_gemm_fp8, grouped_wgrad_fp8, quantize_rows, quantize_weights, swiglu_fp8,
                swiglu_fp8_backward)
+from .experts import _on
 
 
 class _NoSecondDerivative(torch.autograd.Function):
@@ -195,9 +196,10 @@ def gate(logits, num_topk: int, **options):
     """The gate (same options) with gradients of its weights and its balance loss
     towards the logits.  Backward reads the logits, ids, counts, num_valid and
     token_mask again: changing one of them in place before is an error."""
-    _eager_only("gate")
-    kept = []
-    w, loss, _, _ = _Gate.apply(logits, num_topk, options, kept)
+    with _on(logits):
+        _eager_only("gate")
+        kept = []
+        w, loss, _, _ = _Gate.apply(logits, num_topk, options, kept)
     return dataclasses.replace(kept[0], topk_weights=w, loss=loss)
 
 
@@ -245,12 +247,13 @@ def experts(x, topk_idx, topk_weights, w1, w2, num_partitions: int = 1):
     x: bf16 [T, H]; topk_idx, topk_weights: [T, K]; w1: bf16 or fp32 [E, 2 * I, H]
     (gate rows, then up rows), w2: [E, H, I].  Returns bf16 [T, H].  H and I are
     multiples of 128."""
-    _eager_only("experts")
     E = w1.shape[0]
     if w1.dim() != 3 or w2.dim() != 3 or w2.shape[0] != E or w1.shape[1] != 2 * w2.shape[2] or \
             w1.shape[2] != x.shape[1] or w2.shape[1] != x.shape[1]:
         raise ValueError(f"x [T, H], w1 [E, 2 * I, H] and w2 [E, H, I] do not fit: {list(x.shape)}, "
                          f"{list(w1.shape)}, {list(w2.shape)}")
-    layout = _get_dispatch_layout(topk_idx, E, num_partitions)
-    # inside forward gradients are always off
-    return _Experts.apply(x, topk_weights, w1, w2, layout, torch.is_grad_enabled())
+    with _on(x, topk_idx, topk_weights, w1, w2):
+        _eager_only("experts")
+        layout = _get_dispatch_layout(topk_idx, E, num_partitions)
+        # inside forward gradients are always off
+        return _Experts.apply(x, topk_weights, w1, w2, layout, torch.is_grad_enabled())

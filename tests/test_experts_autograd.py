@@ -135,6 +135,7 @@ def _stand_in_layer(monkeypatch, A):
 @pytest.fixture
 def autograd(monkeypatch):
     import combine_get_dispatch_scan_amd.autograd as A
+    monkeypatch.setattr(A, "_on", lambda *t: contextlib.nullcontext(), raising=False)
     monkeypatch.setattr(A, "_eager_only", lambda what: None)
     monkeypatch.setattr(A, "_gate_call", _stand_in_gate)
     monkeypatch.setattr(A, "_gate_backward", _stand_in_gate_backward)
@@ -259,3 +260,37 @@ def test_experts_keeps_what_backward_reads(autograd, monkeypatch, need):
     assert [t.grad is not None for t in (x, w, w1, w2)] == [want_x, want_w, want_1, want_2]
     assert [v for k, v in log if k == "combine_backward"] == [want_w]
     assert sum(k == "wgrad" for k, _ in log) == want_1 + want_2
+
+
+def test_experts_runs_on_its_tensors_device(autograd, monkeypatch):
+    """Every call of the layer, the layout's included, is made with the tensors' device
+    current, and all five tensors have to be on it."""
+    _stand_in_layer(monkeypatch, autograd)
+    given, depth = [], [0]
+
+    @contextlib.contextmanager
+    def on(*tensors):
+        given.append(tensors)
+        depth[0] += 1
+        yield
+        depth[0] -= 1
+
+    monkeypatch.setattr(autograd, "_on", on)
+    for name in ("_get_dispatch_layout", "_dispatch", "quantize_weights", "grouped_gemm_fp8", "swiglu_fp8", "_combine",
+                 "_eager_only"):
+        def call(*a, f=getattr(autograd, name), **k):
+            assert depth[0] == 1
+            return f(*a, **k)
+        monkeypatch.setattr(autograd, name, call)
+    x, idx, w, w1, w2 = _layer_inputs()
+    autograd.experts(x, idx, w, w1, w2)
+    assert [[id(t) for t in g] for g in given] == [[id(t) for t in (x, idx, w, w1, w2)]]
+    assert depth == [0]
+
+
+def test_experts_refuses_cpu_tensors():
+    import combine_get_dispatch_scan_amd.autograd as A
+    with pytest.raises(ValueError, match="expected GPU tensors"):
+        A.experts(*_layer_inputs())
+    with pytest.raises(ValueError, match="expected GPU tensors"):
+        A.gate(torch.zeros(4, 8), 2)
