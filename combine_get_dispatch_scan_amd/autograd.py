@@ -247,9 +247,12 @@ def experts(x, topk_idx, topk_weights, w1, w2, num_partitions: int = 1):
     x: bf16 [T, H]; topk_idx, topk_weights: [T, K]; w1: bf16 or fp32 [E, 2 * I, H]
     (gate rows, then up rows), w2: [E, H, I].  Returns bf16 [T, H].  H and I are
     multiples of 128."""
-    E = w1.shape[0]
-    if w1.dim() != 3 or w2.dim() != 3 or w2.shape[0] != E or w1.shape[1] != 2 * w2.shape[2] or \
-            w1.shape[2] != x.shape[1] or w2.shape[1] != x.shape[1]:
+    if not (x.dim() == 2 and topk_idx.dim() == 2 and topk_idx.shape[0] == x.shape[0] and
+            topk_weights.shape == topk_idx.shape):
+        raise ValueError(f"x [T, H], topk_idx [T, K] and topk_weights [T, K] do not fit: {list(x.shape)}, "
+                         f"{list(topk_idx.shape)}, {list(topk_weights.shape)}")
+    E, H = w1.shape[0], x.shape[1]
+    if not (w1.dim() == 3 and w2.dim() == 3 and w1.shape[1:] == (2 * w2.shape[2], H) and w2.shape[:2] == (E, H)):
         raise ValueError(f"x [T, H], w1 [E, 2 * I, H] and w2 [E, H, I] do not fit: {list(x.shape)}, "
                          f"{list(w1.shape)}, {list(w2.shape)}")
     with _on(x, topk_idx, topk_weights, w1, w2):

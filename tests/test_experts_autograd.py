@@ -294,3 +294,18 @@ def test_experts_refuses_cpu_tensors():
         A.experts(*_layer_inputs())
     with pytest.raises(ValueError, match="expected GPU tensors"):
         A.gate(torch.zeros(4, 8), 2)
+
+
+def test_experts_refuses_choices_that_do_not_fit(autograd, monkeypatch):
+    """Dispatch reads a row of x and a weight for every choice: fewer rows or weights than
+    choices are refused before any call."""
+    log = _stand_in_layer(monkeypatch, autograd)
+    x, idx, w, w1, w2 = _layer_inputs()
+    for bad in ((x[:5], idx, w), (x, idx[:5], w), (x, idx, w[:5]), (x, idx, w[:, :1]), (x, idx[:, 0], w[:, 0]),
+                (x[0], idx, w), (x[None], idx, w)):
+        with pytest.raises(ValueError, match="do not fit"):
+            autograd.experts(*bad, w1, w2)
+    for a, b in ((w1[0], w2), (w1, w2[0]), (w1[:3], w2), (w1[:, :128], w2), (w1[:, :, :64], w2), (w1, w2[:, :64])):
+        with pytest.raises(ValueError, match="do not fit"):
+            autograd.experts(x, idx, w, a, b)
+    assert not log
