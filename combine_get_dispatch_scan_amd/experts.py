@@ -283,11 +283,14 @@ def gate_backward(logits, g: Gate, grad_weights=None, grad_loss=None):
     K = g.topk_idx.shape[1]
     _shape(g.topk_idx, (T, K), "topk_idx")
     _shape(g.num_tokens_per_expert, (E,), "num_tokens_per_expert")
+    _shape(g.num_valid, (1,), "num_valid")
+    if g.token_mask is not None:
+        _shape(g.token_mask, (T,), "token_mask")
     if grad_weights is not None:
         _shape(grad_weights, (T, K), "grad_weights")
     if grad_loss is not None and grad_loss.numel() != 1:
         raise ValueError(f"grad_loss must hold one value, got shape {list(grad_loss.shape)}")
-    with _on(logits, g.topk_idx, grad_weights, grad_loss):
+    with _on(logits, g.topk_idx, g.num_tokens_per_expert, g.num_valid, g.token_mask, grad_weights, grad_loss):
         out = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
         _check(ep_gate_backward(logits.data_ptr(), bf16, ld, T, E, K, g.score, g.normalize, g.scale,
                                 g.balance_coef, _ptr(g.token_mask, "u8", "token_mask"),

@@ -2,6 +2,7 @@
 tensors: the library's calls are replaced by stand-ins on CPU tensors, everything
 around them is the code that runs on the GPU."""
 import contextlib
+import dataclasses
 import gc
 import weakref
 
@@ -309,3 +310,14 @@ def test_experts_refuses_choices_that_do_not_fit(autograd, monkeypatch):
         with pytest.raises(ValueError, match="do not fit"):
             autograd.experts(x, idx, w, a, b)
     assert not log
+
+
+def test_gate_backward_refuses_a_gate_that_does_not_fit(binding):
+    logits = torch.zeros(6, 8)
+    g = binding.gate(logits, 2, token_mask=torch.ones(6, dtype=torch.bool))
+    binding.gate_backward(logits, g)
+    one = torch.zeros(1, dtype=torch.int32)
+    for name, bad in (("topk_idx", g.topk_idx[:5]), ("num_tokens_per_expert", one), ("num_valid", one[:0]),
+                      ("token_mask", g.token_mask[:5])):
+        with pytest.raises(ValueError, match=name):
+            binding.gate_backward(logits, dataclasses.replace(g, **{name: bad}))
