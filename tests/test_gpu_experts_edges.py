@@ -1,6 +1,7 @@
-"""GPU checks of the expert layer where its formulas are hard to hold: sigmoid
-scores far from zero, padding rows on the way back, choices at the ends of their
-range.  Tolerances count roundings as in test_gpu_experts.py."""
+"""GPU checks of the expert layer where its formulas are hard to hold (sigmoid scores
+far from zero, padding rows on the way back, arguments at the ends of their range),
+and of the form of a kernel that a call takes.  Tolerances count roundings as in
+test_gpu_experts.py."""
 import os
 import subprocess
 import sys
@@ -8,7 +9,7 @@ import sys
 import numpy as np
 import pytest
 
-from test_gpu_experts import U, _dev, _gen, _layer_case, _randn
+from test_gpu_experts import U, _check_wgrad, _dev, _gen, _layer_case, _randn
 
 pytestmark = pytest.mark.gpu
 
@@ -154,3 +155,44 @@ def test_expected_rows_at_the_largest_number():
     assert r.returncode == 0, r.stderr[-2000:]
     lines = [l.split()[1] for l in r.stderr.splitlines() if l.startswith("[moe_ep] grouped_gemm")]
     assert lines == ["grouped_gemm_tile"] * 2
+
+
+# ----------------------------------------------------------------------------
+# choice of a form
+# ----------------------------------------------------------------------------
+
+def _launches(calls):
+    """What a child process prints of its expert-layer launches: (kernel, threads of a workgroup)."""
+    _dev()
+    code = (
+        "import sys; sys.path.insert(0, %r)\n"
+        "import torch, combine_get_dispatch_scan_amd as ep\n"
+        "d = torch.device('cuda:0')\n"
+        "def rows(r, k): return torch.zeros((r, k), dtype=torch.uint8, device=d), torch.zeros((r, k // 128), device=d)\n"
+        "def off(g, m): return torch.arange(g + 1, dtype=torch.int32, device=d) * m\n"
+        "%s\ntorch.cuda.synchronize()\n" % (os.path.dirname(os.path.dirname(os.path.abspath(__file__))), calls))
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=100,
+                       env=dict(os.environ, EP_DEBUG="1"))
+    assert r.returncode == 0, r.stderr[-2000:]
+    return [(l.split()[1], int(l.split("block=(")[1].split(",")[0])) for l in r.stderr.splitlines()
+            if l.startswith("[moe_ep] grouped")]
+
+
+def test_form_of_the_weight_gradient():
+    """The smaller tile below 128 rows a group, and up to 128 tiles a group."""
+    got = _launches(
+        "for n, k, m in ((2048, 4096, 600), (2048, 4224, 600), (2048, 4224, 127), (2816, 4096, 128)):\n"
+        "    x, xs = rows(2 * m, k)\n"
+        "    ep.grouped_wgrad_fp8(torch.zeros((2 * m, n), dtype=torch.bfloat16, device=d), x, xs, off(2, m))\n")
+    assert [b for _, b in got] == [256, 512, 256, 512]
+
+
+@pytest.mark.parametrize("N,K", [(2944, 2944), (640, 16384), (16512, 384)])
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+def test_weight_gradient_larger_tile(ep, N, K, dtype):
+    """The larger tile (rows and tiles past the choice above), with partly filled tiles on
+    both sides, stages of one row, groups without rows, and every way rows are laid out."""
+    dt = getattr(torch, dtype)
+    _check_wgrad(ep, [193, 0, 321], N, K, dt)
+    _check_wgrad(ep, [300, 1], N, K, dt, column_major=True)
+    _check_wgrad(ep, [130, 5], N, K, dt, stride=160)
