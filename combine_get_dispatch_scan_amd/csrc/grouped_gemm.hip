@@ -347,20 +347,25 @@ static void skinny_run(const GemmLaunch& L, hipStream_t stream)
 //   16 x 64 skinny  142   164   227   344  1160  4420
 //   32 x 64 skinny  158   176   187   284   787  2890
 //   256 x 256       194   196   197   201   234   570
-// The 64 x 64 skinny form is for products of few large tiles, which leave CUs idle:
-// G = 8, N = 512, K = 1024 at m = 256: 15 us against 25, at 512 (32 tiles): 22 against
-// 26.  At 64 tiles both reach about 0.5 PFLOP/s.
+// The 64 x 64 skinny form is for products of few large tiles, which leave CUs idle: up to
+// 512 of its own tiles (two a CU at once), 64 x 64 against 256 x 256 in us:
+//   64 x 64 tiles    128        256        512        1024       2048
+//   512 x 1024      9 : 15     9 : 16    15 : 18    26 : 25    46 : 25     16 groups at m = 64; 32 at 64 .. 512
+//   512 x 4096     23 : 40    24 : 40    41 : 45    76 : 67   148 : 67     the same
+//   4096 x 7168    36 : 62    37 : 63    67 : 69   128 : 73   254 : 108    2, 4, 8 groups at m = 64; 8 at 128, 256
+// Over 223 cases (1 to 32 groups, m = 17 to 2048) this choice takes 0.5 % longer than the
+// better form; with the border at 704 or 1024 tiles 0.9 %, at 352 4.3 %.
 hipError_t launch_grouped_gemm(const GemmLaunch& L, hipStream_t stream)
 {
     if (L.groups.rows == 0 || L.groups.num == 0)
         return hipSuccess;
     const int m = L.expected_rows;
-    const int64_t tiles = (int64_t)L.groups.num * (((int64_t)m + kTile - 1) / kTile) * ((L.N + kTile - 1) / kTile);
+    const int64_t small = (int64_t)L.groups.num * (((int64_t)m + 63) / 64) * (L.N / 64);    // tiles of 64 x 64
     if (m <= 8) {
         skinny_run<1, 4>(L, stream);
     } else if (m <= 16) {
         skinny_run<2, 4>(L, stream);
-    } else if (tiles < 64) {
+    } else if (small <= 512) {
         skinny_run<4, 4>(L, stream);
     } else {
         debug_launch("grouped_gemm_tile", dim3(kCus), dim3(512), 0);

@@ -196,3 +196,16 @@ def test_weight_gradient_larger_tile(ep, N, K, dtype):
     _check_wgrad(ep, [193, 0, 321], N, K, dt)
     _check_wgrad(ep, [300, 1], N, K, dt, column_major=True)
     _check_wgrad(ep, [130, 5], N, K, dt, stride=160)
+
+
+def test_form_of_the_product():
+    """By the typical rows of a group up to 16, then 64 x 64 tiles up to 512 of them."""
+    got = _launches(
+        "for g, n, m in ((4, 256, 8), (4, 256, 16), (4, 256, 17), (32, 512, 128), (32, 512, 129), (16, 4096, 32)):\n"
+        "    x, xs = rows(g * m, 256)\n"
+        "    w, ws = torch.zeros((g, n, 256), dtype=torch.uint8, device=d), torch.zeros((g, n // 128, 2), device=d)\n"
+        "    for e in (m, 0):\n"
+        "        ep.grouped_gemm_fp8(x, xs, w, ws, off(g, m), expected_rows=e)\n")
+    # (the skinny forms share their name)
+    want = ["grouped_gemm_skinny"] * 4 + ["grouped_gemm_tile"] * 2
+    assert [k for k, _ in got] == [k for k in want for _ in (0, 1)]
