@@ -209,3 +209,69 @@ def test_form_of_the_product():
     # (the skinny forms share their name)
     want = ["grouped_gemm_skinny"] * 4 + ["grouped_gemm_tile"] * 2
     assert [k for k, _ in got] == [k for k in want for _ in (0, 1)]
+
+
+# ----------------------------------------------------------------------------
+# autograd
+# ----------------------------------------------------------------------------
+
+def test_training_steps_keep_no_memory(ep):
+    """What is allocated after a step of gate and experts is what was before it."""
+    import gc
+
+    import combine_get_dispatch_scan_amd.autograd as A
+    x, logits, w1, w2 = _layer_case(40, T=500)
+    mask = torch.rand(500, generator=_gen(41), device=x.device) > 0.1
+    params = [t.requires_grad_() for t in (logits, w1, w2)]
+
+    def step(backward):
+        g = A.gate(logits, 2, balance_coef=0.1, token_mask=mask)
+        out = A.experts(x, g.topk_idx, g.topk_weights, w1, w2)
+        if backward:
+            (out.float().square().mean() + g.loss.sum()).backward()
+            for p in params:
+                p.grad = None
+
+    sizes = []
+    for i in range(8):
+        step(backward=i % 2 == 0)
+        gc.collect()
+        sizes.append(torch.cuda.memory_allocated())
+    assert len(set(sizes[1:])) == 1, sizes
+
+
+def test_changes_between_forward_and_backward(ep):
+    import combine_get_dispatch_scan_amd.autograd as A
+    x, logits, w1, w2 = _layer_case(42)
+    logits.requires_grad_()
+    mask = torch.ones(len(x), dtype=torch.bool, device=x.device)
+    for change in (lambda g: mask.fill_(0), lambda g: g.num_tokens_per_expert.zero_(), lambda g: g.topk_idx.fill_(0)):
+        mask.fill_(1)
+        g = A.gate(logits, 2, balance_coef=0.1, token_mask=mask)
+        change(g)
+        with pytest.raises(RuntimeError, match="inplace"):
+            g.loss.sum().backward()
+    mask.fill_(1)
+    g = A.gate(logits, 2, balance_coef=0.1, token_mask=mask)
+    g.loss.mul_(2.0).sum().backward()
+    one = torch.ones(1, device=x.device)
+    assert torch.equal(logits.grad, ep.gate_backward(logits.detach(), ep.gate(logits.detach(), 2, balance_coef=0.1),
+                                                     None, 2 * one))
+    # a second derivative is refused, the first one under create_graph is not
+    out = A.experts(x.requires_grad_(), g.topk_idx, g.topk_weights.detach(), w1, w2)
+    first, = torch.autograd.grad(out.float().sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError, match="no second derivative"):
+        first.float().square().sum().backward()
+
+
+def test_inference_with_parameters(ep):
+    """The same bits without gradients, and no more memory than the forward pass needs."""
+    import combine_get_dispatch_scan_amd.autograd as A
+    x, logits, w1, w2 = _layer_case(43, T=300)
+    g = ep.gate(logits, 2)
+    want = A.experts(x, g.topk_idx, g.topk_weights, w1, w2)
+    w1, w2 = torch.nn.Parameter(w1), torch.nn.Parameter(w2)
+    assert torch.equal(A.experts(x, g.topk_idx, g.topk_weights, w1, w2), want)
+    for mode in (torch.no_grad, torch.inference_mode):
+        with mode():
+            assert torch.equal(A.experts(x, g.topk_idx, g.topk_weights, w1, w2), want)
