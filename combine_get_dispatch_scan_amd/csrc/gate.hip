@@ -15,8 +15,8 @@
 // done.  The workgroups' sums are then added in their order by a second launch, so
 // the loss does not depend on timing (a few tokens take one workgroup and one launch).
 //
-// 16384 x 256 bf16 logits, top-8 (MI355X): 15.4 us and 6.9 for the second launch,
-// the backward pass 12.5.  The 19 MB they move take 4 us at the rate of a large
+// 16384 x 256 bf16 logits, top-8 (MI355X): 15.0 us and 7.0 for the second launch,
+// the backward pass 12.7.  The 19 MB they move take 4 us at the rate of a large
 // copy; the rounds' instructions bound the first, the wait for the 256 workgroups'
 // sums (512 KB by one CU) the second, the scores' exponentials and divisions the
 // backward pass.
@@ -356,9 +356,9 @@ __global__ __launch_bounds__(kGateThreads) void gate_kernel(GateLaunch a)
 
 // Launch shape.  A token's rounds are a chain of about 800 instructions, so tokens
 // are spread over the SIMDs before any SIMD gets a second wave to fill its waits:
-// 128 tokens, 256 experts, top-8 take 9.0 + 3.4 us in 32 workgroups of one wave and
-// the second launch, 24.4 in one workgroup of 16 waves; 16384 tokens 15.4 + 6.9 in
-// 256 of 16 waves and 34.2 + 8.9 in 256 of four.  16 tokens (of 16 lanes) go
+// 128 tokens, 256 experts, top-8 of sigmoid scores take 10.3 + 3.6 us in 32 workgroups
+// of one wave and the second launch, 28.5 in one workgroup of 16 waves; 16384 tokens
+// (softmax) 15.0 + 7.0 in 256 of 16 waves and 34.2 + 8.9 in 256 of four.  16 tokens (of 16 lanes) go
 // in one workgroup without a second launch.
 struct GateShape {
     int threads, blocks;

@@ -123,14 +123,14 @@ __global__ __launch_bounds__(256) void gemm_skinny_kernel(GemmLaunch a)
 // which global chunk lands where), so that eight rows read at the same chunk
 // hit all banks once.
 //
-// 65536 rows in 32 groups, N = 4096, K = 7168: 1836-1876 us, 2.05-2.10 PFLOP/s, where a library
-// product of E4M3 matrices with one scale reaches 2.9 (8192^3) to 3.2 (16384^3).  The
-// matrix cores are busy for half of the time.  Taken apart: the copies alone
-// take 1320-1400 us (two stages in flight; 1830 us with one, as here, when nothing is
-// computed meanwhile), the matrix instructions and scaled sums alone 1290 us, with
-// the LDS reads 1390 us; together they do not overlap fully, and the clock falls with
-// the load (2.4 GHz to 2.0).  Forms with a stream of stages across tiles, copies one
-// and a half stages ahead, or pinned fetches into L2 came out within 3% or slower.
+// 65536 rows in 32 groups, N = 4096, K = 7168: 1838-1899 us over five inputs and three
+// runs, about 2.05 PFLOP/s, where a library product of E4M3 matrices with one scale
+// reaches 2.9 (8192^3) to 3.2 (16384^3).  The matrix cores are busy for 51% of the
+// cycles, and the clock falls to 1.9 GHz.  In a run at 1883 us, copies of the kernel with
+// parts taken out take 1612 us (no matrix instructions, scaled sums and LDS reads) and
+// 1442 us (no copies after the first two blocks): the two do not overlap fully.  Forms
+// with a stream of stages across tiles, copies one and a half stages ahead, or pinned
+// fetches into L2 came out within 3% or slower.
 constexpr int kTile = 256;
 constexpr int kStage = kTile * kQBlock;
 

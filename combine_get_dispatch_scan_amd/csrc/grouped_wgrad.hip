@@ -3,8 +3,11 @@
 // with dy in bf16 and x in the 8 bits it was dispatched in (the activation
 // checkpoint of the product).  The scale belongs to a row, and rows are what is
 // summed over, so it cannot be taken out of the sum: x is widened to bf16 on its
-// way into LDS (a 4-bit code times the scale, one rounding of 2^-9 relative) and
-// the product runs on the bf16 matrix cores with fp32 sums.
+// way into LDS (an 8-bit code times the scale in fp32, then one rounding by at most
+// 2^-8 of the value, which is 1.7e-3 of the result's norm: with an out of bf16 as much
+// as its own rounding, with one of fp32 all of the error) and the product runs on the
+// bf16 matrix cores with fp32 sums.  fp32 products of the same numbers would cost the
+// matrix cores sixteen times as much.
 #include "expert_launch.h"
 #include "mfma.h"
 
@@ -19,14 +22,15 @@ namespace moe_ep {
 // number, so that the rows it spans lie in different banks.
 //
 // Two forms (G = 32, N = 4096, K = 7168, MI355X):
-//   NW = 2, 64 rows   one workgroup a CU; 2265 us at 1024 rows a group (850 TFLOP/s),
-//                     681 us at 128, 514 us at 16
+//   NW = 2, 64 rows   one workgroup a CU; 2262 us at 1024 rows a group (850 TFLOP/s),
+//                     682 us at 128, 514 us at 16
 //   NW = 1, 32 rows   two, so that one's first loads and last stores run beside the
-//                     other's products: 429 us at 16 rows a group, 698 us at 128,
-//                     2582 us at 1024
-// What bounds the first is the time a stage's loads take to arrive (with the matrix
-// instructions taken out it still takes 1923 us) and the stores at a tile's end
-// (385 us of it); the second, with few rows, the stores: 1.9 GB of gradients.
+//                     other's products: 429 us at 16 rows a group, 699 us at 128,
+//                     2603 us at 1024
+// What bounds the first is the time a stage's loads take to arrive (a copy without the
+// matrix instructions takes 1916 us in a run at 2264) and the stores at a tile's end (one
+// without them 1930); the matrix cores are busy for 37% of the cycles.  The second, with
+// few rows, is bound by the stores: 1.9 GB of gradients.
 constexpr int kTile = 256;                     // columns of x
 
 // The permutation of row r's chunks: rows 0-3 and 8-11 (4-7 and 12-15), which the
@@ -43,7 +47,7 @@ __device__ __forceinline__ bf16x8 read_chunk(const uint16_t* lds, int row, int c
     return __builtin_bit_cast(bf16x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
-// 64 rows: the wave's 8 tiles of dy's columns x 4 of x's.
+// ROWS rows: the wave's 8 tiles of dy's columns x 4 of x's.
 template <int NW, int ROWS>
 __device__ __forceinline__ void wgrad_stage(const uint16_t* ly, const uint16_t* lx, int wn, int wk, int lane,
                                             f32x4 (&acc)[8][4])

@@ -3,7 +3,7 @@
 // for the backward product).  The arithmetic is dispatch's: a = max(amax, 2^-64),
 // codes = RNE_E4M3FN(x * (448 / a)), scale = a / 448, one fp32 rounding each.  Both
 // are bound by HBM: 32768 x 7168 rows in 125 us (5.7 TB/s), 32 x 4096 x 7168 bf16
-// weights with their transposes in 714 us (5.3 TB/s; a 1 GiB copy: 5.05).
+// weights with their transposes in 720 us (5.2 TB/s; a 1 GiB copy: 5.05).
 #include "expert_launch.h"
 #include "quant16.h"
 

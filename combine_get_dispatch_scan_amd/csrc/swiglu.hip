@@ -13,7 +13,7 @@
 // division its reciprocal (1 ulp).  Both passes are bound by HBM: every value is
 // read and written once.  Eight lanes hold one 128-channel block of g and the
 // block of u that belongs to it.  32768 rows, inner = 2048 (MI355X): forward with
-// checkpoint 83 us, backward with both outputs 124 us, 5.7 and 5.5 TB/s of the bytes
+// checkpoint 84 us, backward with both outputs 124 us, 5.7 and 5.5 TB/s of the bytes
 // they cannot do without (a 1 GiB copy: 5.05).
 #include "expert_launch.h"
 #include "quant16.h"
