@@ -30,8 +30,8 @@ calls.
 Only argument marshalling happens here; every step runs in the HIP kernels.
 These functions are for eager autograd: a backward pass captured into a graph
 while an eager graph of the same leaves is alive ends the process in torch, so
-``gate`` and ``experts`` refuse to be captured (the plain calls they are made of
-can be).  None of them has a second derivative: asking for one raises.
+``gate`` and ``experts`` refuse to be captured, forward and backward (the plain
+calls they are made of can be).  None of them has a second derivative: asking for one raises.
 """
 from __future__ import annotations
 
@@ -183,6 +183,7 @@ class _Gate(torch.autograd.Function):
     @staticmethod
     @_first_order
     def backward(ctx, grad_weights, grad_loss, *_):
+        _eager_only("the backward pass of gate")
         logits, idx, counts, valid, mask = ctx.saved_tensors
         if grad_weights is not None:
             grad_weights = grad_weights.contiguous()
@@ -224,10 +225,12 @@ class _Experts(torch.autograd.Function):
     @staticmethod
     @_first_order
     def backward(ctx, grad_out):
+        _eager_only("the backward pass of experts")
         x8, xs, a8, a_s, c8, cs, y2, w1t, s1t, w2t, s2t = ctx.saved_tensors
         h = ctx.handle
         want_x, want_w, want_1, want_2 = ctx.needs_input_grad[:4]
-        gy, gw = _combine_backward(grad_out.contiguous(), h, y=y2 if want_w else None)     # dispatch's copy of the weights
+        # with dispatch's copy of the weights
+        gy, gw = _combine_backward(grad_out.contiguous(), h, y=y2 if want_w else None)
         gx = g1 = g2 = None
         if want_2:
             g2 = grouped_wgrad_fp8(gy, a8, a_s, h, out_dtype=ctx.dtypes[1])

@@ -321,3 +321,23 @@ def test_gate_backward_refuses_a_gate_that_does_not_fit(binding):
                       ("token_mask", g.token_mask[:5])):
         with pytest.raises(ValueError, match=name):
             binding.gate_backward(logits, dataclasses.replace(g, **{name: bad}))
+
+
+def test_backward_is_not_captured_either(autograd, monkeypatch):
+    """A backward pass captured while its forward pass was eager is refused before any call."""
+    log = _stand_in_layer(monkeypatch, autograd)
+    x, idx, w, w1, w2 = _layer_inputs()
+    out = autograd.experts(x.requires_grad_(), idx, w, w1, w2)
+    logits = torch.randn(6, 8, requires_grad=True)
+    g = autograd.gate(logits, 2, balance_coef=0.1)
+
+    def capturing(what):
+        raise RuntimeError(f"{what} cannot be captured into a graph")
+
+    monkeypatch.setattr(autograd, "_eager_only", capturing)
+    n = len(log)
+    with pytest.raises(RuntimeError, match="cannot be captured"):
+        out.sum().backward()
+    with pytest.raises(RuntimeError, match="cannot be captured"):
+        g.loss.sum().backward()
+    assert len(log) == n and x.grad is None and logits.grad is None
