@@ -243,7 +243,8 @@ hipError_t launch_grouped_wgrad(const WgradLaunch& L, hipStream_t stream)
     // m: rows a group on average; tiles: 256 x 256 ones of one group.  With equal groups and
     // every CU busy the forms cross near 128 rows.  Groups differ in size, which the host does
     // not know, and a launch ends with its largest group's tiles: where those leave half of
-    // the CUs idle, twice as many smaller ones end sooner.  NW = 1 against NW = 2 in us, 16
+    // the CUs idle, twice as many smaller ones end sooner; from 512 rows a group only while
+    // all groups' tiles do not fill the CUs twice, since equal groups lose more there.  NW = 1 against NW = 2 in us, 16
     // groups, even sizes | zipf ones, (rank + 1)^-1.2:
     //   m                                128                         512                        1024
     //   1408 x 2048 (48)     33 : 35 |  36 : 47       76 :  69 |  103 :  116      127 :  115 |  193 :  218
@@ -251,10 +252,10 @@ hipError_t launch_grouped_wgrad(const WgradLaunch& L, hipStream_t stream)
     //   2816 x 4096 (176)   130 : 129 | 138 : 142    293 : 271 |  322 :  305      491 :  441 |  525 :  508
     //   4096 x 7168 (448)   355 : 346 | 365 : 348    773 : 702 |  777 :  705     1289 : 1133 | 1297 : 1141
     // Over 572 cases (1 to 64 groups, 8 to 448 tiles, 48 to 2048 rows, both distributions) this
-    // choice takes 1.6 % longer than the better form, always NW = 1 3.2 %, always NW = 2 7.5 %.
+    // choice takes 1.5 % longer than the better form, always NW = 1 3.2 %, always NW = 2 7.5 %.
     const int m = L.groups.rows / L.groups.num;
     const int64_t tiles = (int64_t)((L.N + kTile - 1) / kTile) * ((L.K + kTile - 1) / kTile);
-    if (m < 128 || tiles <= 128)
+    if (m < 128 || (tiles <= 128 && (m < 512 || tiles * L.groups.num < 512)))
         wgrad_run<1, 32>(L, stream);
     else
         wgrad_run<2, 64>(L, stream);

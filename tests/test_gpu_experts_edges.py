@@ -179,12 +179,14 @@ def _launches(calls):
 
 
 def test_form_of_the_weight_gradient():
-    """The smaller tile below 128 rows a group, and up to 128 tiles a group."""
+    """The smaller tile below 128 rows a group, and up to 128 tiles a group; from 512 rows on
+    only below 512 tiles in all."""
     got = _launches(
-        "for n, k, m in ((2048, 4096, 600), (2048, 4224, 600), (2048, 4224, 127), (2816, 4096, 128)):\n"
-        "    x, xs = rows(2 * m, k)\n"
-        "    ep.grouped_wgrad_fp8(torch.zeros((2 * m, n), dtype=torch.bfloat16, device=d), x, xs, off(2, m))\n")
-    assert [b for _, b in got] == [256, 512, 256, 512]
+        "for g, n, k, m in ((2, 2048, 4096, 600), (2, 2048, 4224, 600), (2, 2048, 4224, 127), (2, 2816, 4096, 128),\n"
+        "                   (4, 2048, 4096, 511), (4, 2048, 4096, 512)):\n"
+        "    x, xs = rows(g * m, k)\n"
+        "    ep.grouped_wgrad_fp8(torch.zeros((g * m, n), dtype=torch.bfloat16, device=d), x, xs, off(g, m))\n")
+    assert [b for _, b in got] == [256, 512, 256, 512, 256, 512]
 
 
 @pytest.mark.parametrize("N,K", [(2944, 2944), (640, 16384), (16512, 384)])
