@@ -358,8 +358,8 @@ __global__ __launch_bounds__(kGateThreads) void gate_kernel(GateLaunch a)
 // are spread over the SIMDs before any SIMD gets a second wave to fill its waits:
 // 128 tokens, 256 experts, top-8 of sigmoid scores take 10.3 + 3.6 us in 32 workgroups
 // of one wave and the second launch, 28.5 in one workgroup of 16 waves; 16384 tokens
-// (softmax) 15.0 + 7.0 in 256 of 16 waves and 34.2 + 8.9 in 256 of four.  16 tokens (of 16 lanes) go
-// in one workgroup without a second launch.
+// (softmax) 15.0 + 7.0 in 256 of 16 waves and 34.2 + 8.9 in 256 of four.  16 tokens (of
+// 16 lanes) go in one workgroup without a second launch.
 struct GateShape {
     int threads, blocks;
 };

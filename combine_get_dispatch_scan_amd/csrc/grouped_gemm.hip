@@ -123,9 +123,9 @@ __global__ __launch_bounds__(256) void gemm_skinny_kernel(GemmLaunch a)
 // which global chunk lands where), so that eight rows read at the same chunk
 // hit all banks once.
 //
-// 65536 rows in 32 groups, N = 4096, K = 7168: 1838-1899 us over five inputs and three
-// runs, about 2.05 PFLOP/s, where a library product of E4M3 matrices with one scale
-// reaches 2.9 (8192^3) to 3.2 (16384^3).  The matrix cores are busy for 51% of the
+// 65536 rows in 32 groups, N = 4096, K = 7168: 1838-1899 us over five inputs on one card,
+// 1949 on another, 1.97-2.09 PFLOP/s, where a library product of E4M3 matrices with one
+// scale reaches 2.9 (8192^3) to 3.2 (16384^3).  The matrix cores are busy for 51% of the
 // cycles, and the clock falls to 1.9 GHz.  In a run at 1883 us, copies of the kernel with
 // parts taken out take 1612 us (no matrix instructions, scaled sums and LDS reads) and
 // 1442 us (no copies after the first two blocks): the two do not overlap fully.  Forms
