@@ -279,7 +279,8 @@ def _kinds():
         import torch
         _KINDS.update(bf16=(torch.bfloat16,), fp8=(torch.float8_e4m3fn, torch.uint8),
                       f32=(torch.float32,), i64=(torch.int64,), i32=(torch.int32,),
-                      u8=(torch.uint8,))
+                      u8=(torch.uint8,), fp4=(torch.uint8, torch.float4_e2m1fn_x2),
+                      e8m0=(torch.float8_e8m0fnu, torch.uint8))
     return _KINDS
 
 
@@ -638,3 +639,14 @@ from .experts import (  # noqa: E402
     ep_gate_workspace_bytes, ep_grouped_gemm_fp8, ep_grouped_wgrad_fp8, ep_quantize_rows,
     ep_quantize_weights, ep_swiglu_fp8, ep_swiglu_fp8_backward, gate, gate_backward, grouped_gemm_fp8,
     grouped_wgrad_fp8, quantize_rows, quantize_weights, swiglu_fp8, swiglu_fp8_backward)
+
+
+# ----------------------------------------------------------------------------
+# around the expert layer: norms before and after a block, 4-bit expert weights
+# ----------------------------------------------------------------------------
+
+from .block import (  # noqa: E402
+    EP_GATE_CHANNEL, EP_GATE_NONE, EP_GATE_TOKEN, BlockNorm, BlockNormGrads, Fp4Weights, block_norm,
+    block_norm_backward, dequantize_weights_fp4, ep_block_norm, ep_block_norm_backward, ep_block_norm_t,
+    ep_block_norm_workspace_bytes, ep_dequantize_weights_fp4, ep_grouped_gemm_fp4,
+    ep_quantize_weights_fp4, grouped_gemm_fp4, quantize_weights_fp4)

@@ -1,0 +1,578 @@
+// The norms before and after a block with its gate and residual scales, on gfx950:
+//   z  = y * rz,  rz = 1 / sqrt(mean y^2 + eps)      (or z = y)
+//   x' = a x + fy gt z,  fy = b * channel gate * (o + y_weight),  gt = token gate
+//   h  = x' r (o + weight),  r = 1 / sqrt(mean x'^2 + eps),  as bf16 and as FP8 rows
+// and their gradients.  A team of lanes (a wave, or a workgroup of up to 16) holds a
+// row in registers, so every value is read and written once; means are fp32 sums
+// over the lanes.  All arithmetic is fp32, and every output is rounded once.
+#include "block_launch.h"
+#include "quant16.h"
+
+namespace moe_ep {
+
+constexpr int kTeamWaves = 16;               // waves of a row, at most
+constexpr int kForwardBlocks = 2048;
+constexpr int kBackwardBlocks = 512;
+
+template <int CTRL>
+__device__ __forceinline__ float dpp_f(float v)
+{
+    return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), CTRL, 0xF, 0xF, true));
+}
+
+// Sum over a wave's lanes, the same in all of them: lane ^ 1, lane ^ 2, the other four
+// of eight, the other eight of sixteen, then the four sixteens.
+__device__ __forceinline__ float wave_sum(float v)
+{
+    v += dpp_f<0xB1>(v);
+    v += dpp_f<0x4E>(v);
+    v += dpp_f<0x141>(v);
+    v += dpp_f<0x140>(v);
+    return (readlane_f(v, 0) + readlane_f(v, 16)) + (readlane_f(v, 32) + readlane_f(v, 48));
+}
+
+__device__ __forceinline__ float max16(float m)
+{
+    m = max8(m);
+    return fmaxf(m, dpp_f<0x140>(m));
+}
+
+// Sums over the team.  A workgroup's waves meet in LDS, in slots that are used in turn:
+// a slot is written again only after the barrier of the sum in between.
+template <bool WAVE, int N>
+struct TeamSum {
+    float (*slots)[kTeamWaves][N];
+    int turn;
+
+    __device__ __forceinline__ void operator()(float (&v)[N])
+    {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            v[i] = wave_sum(v[i]);
+        if (WAVE)
+            return;
+        const int wave = threadIdx.x / kWave, waves = blockDim.x / kWave;
+        if (threadIdx.x % kWave == 0)
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                slots[turn][wave][i] = v[i];
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            v[i] = slots[turn][0][i];
+        for (int w = 1; w < waves; ++w)
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                v[i] += slots[turn][w][i];
+        turn ^= 1;
+    }
+};
+
+// Eight channels of a vector of parameters.
+__device__ __forceinline__ void load_param8(const void* p, bool f32, int vec, float (&v)[8])
+{
+    if (f32) {
+        const u32x4 a = load16_hint<false>(static_cast<const float*>(p) + 8 * vec);
+        const u32x4 b = load16_hint<false>(static_cast<const float*>(p) + 8 * vec + 4);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            v[j] = __uint_as_float(a[j]);
+            v[4 + j] = __uint_as_float(b[j]);
+        }
+    } else {
+        const u32x4 a = load16_hint<false>(static_cast<const uint16_t*>(p) + 8 * vec);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            v[2 * j] = bf16_lo(a[j]);
+            v[2 * j + 1] = bf16_hi(a[j]);
+        }
+    }
+}
+
+__device__ __forceinline__ float load_param(const void* p, bool f32, int i)
+{
+    if (f32)
+        return static_cast<const float*>(p)[i];
+    return __uint_as_float((uint32_t)static_cast<const uint16_t*>(p)[i] << 16);
+}
+
+__device__ __forceinline__ void store_param(void* p, bool f32, int i, float v)
+{
+    if (f32)
+        static_cast<float*>(p)[i] = v;
+    else
+        static_cast<uint16_t*>(p)[i] = (uint16_t)f32_to_bf16_rne(v);
+}
+
+// Factors of y and of the norm in eight channels.
+__device__ __forceinline__ void y_factors(const ep_block_norm_t& a, int vec, float (&f)[8])
+{
+    float t[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        f[j] = a.y_scale;
+    if (a.y_weight) {
+        load_param8(a.y_weight, a.weights_f32, vec, t);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            f[j] *= a.weight_offset + t[j];
+    }
+    if (a.gate_kind == EP_GATE_CHANNEL) {
+        load_param8(a.gate, a.gate_f32, vec, t);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            f[j] *= t[j];
+    }
+}
+
+__device__ __forceinline__ void norm_factors(const ep_block_norm_t& a, int vec, float (&f)[8])
+{
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        f[j] = 1.0f;
+    if (a.weight) {
+        load_param8(a.weight, a.weights_f32, vec, f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            f[j] += a.weight_offset;
+    }
+}
+
+// Eight values of a row as they lie in memory: bf16 or fp32.
+template <bool F32>
+struct Raw8 {
+    u32x4 d[F32 ? 2 : 1];
+
+    __device__ __forceinline__ void zero()
+    {
+#pragma unroll
+        for (int i = 0; i < (F32 ? 2 : 1); ++i)
+            d[i] = u32x4{0u, 0u, 0u, 0u};
+    }
+    __device__ __forceinline__ void load(const void* p, size_t at)
+    {
+        const char* q = static_cast<const char*>(p) + at * (F32 ? 4 : 2);
+#pragma unroll
+        for (int i = 0; i < (F32 ? 2 : 1); ++i)
+            d[i] = load16_hint<false>(q + 16 * i);
+    }
+    __device__ __forceinline__ float get(int j) const
+    {
+        if (F32)
+            return __uint_as_float(d[F32 ? j >> 2 : 0][j & 3]);
+        return (j & 1) ? bf16_hi(d[0][j >> 1]) : bf16_lo(d[0][j >> 1]);
+    }
+    static __device__ __forceinline__ void store(void* p, size_t at, const float (&v)[8])
+    {
+        char* q = static_cast<char*>(p) + at * (F32 ? 4 : 2);
+        if (F32) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                store16_hint<false>(q + 16 * i, u32x4{__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]),
+                                                      __float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3])});
+        } else {
+            u32x4 o;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                o[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
+            store16_hint<false>(q, o);
+        }
+    }
+};
+
+template <bool WAVE, int V, bool F32, int THREADS>
+__global__ __launch_bounds__(THREADS) void block_norm_kernel(BlockNormLaunch L)
+{
+    __shared__ float slots[2][kTeamWaves][1];
+    const ep_block_norm_t& a = L.in;
+    const int lane = WAVE ? threadIdx.x % kWave : threadIdx.x, lanes = WAVE ? kWave : blockDim.x;
+    const int H = a.width, vecs = H / 8;
+    const int teams = WAVE ? gridDim.x * (THREADS / kWave) : gridDim.x;
+    const int first = WAVE ? blockIdx.x * (THREADS / kWave) + threadIdx.x / kWave : blockIdx.x;
+    const float inv = 1.0f / (float)H;
+    TeamSum<WAVE, 1> sum{slots, 0};
+    float fy[V][8], fw[V][8];
+    bool on[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        on[i] = lane + i * lanes < vecs;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            fy[i][j] = fw[i][j] = 0.0f;
+        if (on[i]) {
+            if (a.y)
+                y_factors(a, lane + i * lanes, fy[i]);
+            norm_factors(a, lane + i * lanes, fw[i]);
+        }
+    }
+    for (int64_t row = first; row < a.num_rows; row += teams) {
+        Raw8<F32> x[V];
+        Raw8<false> y[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            x[i].zero();
+            y[i].zero();
+            if (on[i]) {
+                const int c = (lane + i * lanes) * 8;
+                x[i].load(a.x, row * a.x_ld + c);
+                if (a.y)
+                    y[i].load(a.y, row * a.y_ld + c);
+            }
+        }
+        float v[V][8];
+        float ss[1] = {0.0f};
+        if (a.y) {
+            float cy = 1.0f;
+            if (a.y_norm) {
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        ss[0] = __builtin_fmaf(y[i].get(j), y[i].get(j), ss[0]);
+                sum(ss);
+                cy = __builtin_amdgcn_rsqf(ss[0] * inv + a.eps);
+            }
+            if (a.gate_kind == EP_GATE_TOKEN)
+                cy *= load_param(a.gate, a.gate_f32, (int)row);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    v[i][j] = __builtin_fmaf(a.residual_scale, x[i].get(j), y[i].get(j) * cy * fy[i][j]);
+                if (L.xo && on[i])
+                    Raw8<F32>::store(L.xo, row * H + (lane + i * lanes) * 8, v[i]);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    v[i][j] = x[i].get(j);
+        }
+        if (!a.norm)
+            continue;
+        ss[0] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                ss[0] = __builtin_fmaf(v[i][j], v[i][j], ss[0]);
+        sum(ss);
+        const float r = __builtin_amdgcn_rsqf(ss[0] * inv + a.eps);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int vec = lane + i * lanes;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                v[i][j] = v[i][j] * r * fw[i][j];
+            if (L.h && on[i])
+                Raw8<false>::store(L.h, row * H + vec * 8, v[i]);
+            if (L.codes) {
+                // sixteen lanes hold a block of 128 (all of them on, or none)
+                float m = 0.0f;
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    m = fmaxf(m, fabsf(v[i][j]));
+                const float top = fmaxf(max16(m), 0x1p-64f);
+                const float k = 448.0f / top;
+                uint32_t q[2];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    q[j] = e4m3fn_pair<false>(v[i][4 * j] * k, v[i][4 * j + 1] * k, 0u);
+                    q[j] = e4m3fn_pair<true>(v[i][4 * j + 2] * k, v[i][4 * j + 3] * k, q[j]);
+                }
+                if (on[i]) {
+                    *reinterpret_cast<uint2*>(L.codes + row * H + vec * 8) = uint2{q[0], q[1]};
+                    if ((vec & 15) == 0)
+                        L.scales[row * (H / kQBlock) + vec / 16] = top / 448.0f;
+                }
+            }
+        }
+    }
+}
+
+// Backward.  Both factors of the row are computed again from x and y, so nothing but
+// the inputs is kept between the passes:
+//   d = gh (o + weight),  g = gx + r (d - x' r * mean(d x' r)),   dx = a g
+//   s = sum over channels of g fy z  (the token gate's gradient)
+//   dy = rz gt (g fy - z s / width)   (without y's norm: gt g fy)
+//   dweight = sum over rows of gh x' r;  S = sum over rows of gt g z, from which
+//   dy_weight = b * channel gate * S and the channel gate's gradient b (o + y_weight) S
+// The sums over rows stay in the registers of the workgroups, which take rows in a
+// fixed order, and are added by a second launch.
+template <bool WAVE, int V, bool F32, int THREADS>
+__global__ __launch_bounds__(THREADS) void block_norm_backward_kernel(BlockNormBackwardLaunch L)
+{
+    __shared__ float slots[2][kTeamWaves][2];
+    extern __shared__ float comb[];             // WAVE: [2][width], where the waves' sums meet
+    const ep_block_norm_t& a = L.in;
+    const int lane = WAVE ? threadIdx.x % kWave : threadIdx.x, lanes = WAVE ? kWave : blockDim.x;
+    const int H = a.width, vecs = H / 8;
+    const int teams = WAVE ? gridDim.x * (THREADS / kWave) : gridDim.x;
+    const int first = WAVE ? blockIdx.x * (THREADS / kWave) + threadIdx.x / kWave : blockIdx.x;
+    const float inv = 1.0f / (float)H;
+    TeamSum<WAVE, 2> sum{slots, 0};
+    float fy[V][8], fw[V][8], P[V][8], S[V][8];
+    bool on[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        on[i] = lane + i * lanes < vecs;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            fy[i][j] = fw[i][j] = P[i][j] = S[i][j] = 0.0f;
+        if (on[i]) {
+            if (a.y)
+                y_factors(a, lane + i * lanes, fy[i]);
+            if (a.norm)
+                norm_factors(a, lane + i * lanes, fw[i]);
+        }
+    }
+    for (int64_t row = first; row < a.num_rows; row += teams) {
+        Raw8<F32> x[V], gx[V];
+        Raw8<false> y[V], gh[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            x[i].zero();
+            y[i].zero();
+            gx[i].zero();
+            gh[i].zero();
+            if (on[i]) {
+                const int c = (lane + i * lanes) * 8;
+                x[i].load(a.x, row * a.x_ld + c);
+                if (a.y)
+                    y[i].load(a.y, row * a.y_ld + c);
+                if (L.gx)
+                    gx[i].load(L.gx, row * H + c);
+                if (L.gh)
+                    gh[i].load(L.gh, row * H + c);
+            }
+        }
+        float rz = 1.0f, gt = 1.0f;
+        if (a.y_norm) {
+            float ss[2] = {0.0f, 0.0f};
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    ss[0] = __builtin_fmaf(y[i].get(j), y[i].get(j), ss[0]);
+            sum(ss);
+            rz = __builtin_amdgcn_rsqf(ss[0] * inv + a.eps);
+        }
+        if (a.gate_kind == EP_GATE_TOKEN)
+            gt = load_param(a.gate, a.gate_f32, (int)row);
+        float g[V][8];
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                g[i][j] = gx[i].get(j);
+        if (L.gh) {
+            float v[V][8];
+            float ss[2] = {0.0f, 0.0f};
+            const float cy = rz * gt;
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    v[i][j] = a.y ? __builtin_fmaf(a.residual_scale, x[i].get(j), y[i].get(j) * cy * fy[i][j])
+                                  : x[i].get(j);
+                    ss[0] = __builtin_fmaf(v[i][j], v[i][j], ss[0]);
+                    ss[1] = __builtin_fmaf(gh[i].get(j) * fw[i][j], v[i][j], ss[1]);
+                }
+            sum(ss);
+            const float r = __builtin_amdgcn_rsqf(ss[0] * inv + a.eps);
+            const float k = r * ss[1] * inv;
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float xh = v[i][j] * r;
+                    P[i][j] = __builtin_fmaf(gh[i].get(j), xh, P[i][j]);
+                    g[i][j] = __builtin_fmaf(r, gh[i].get(j) * fw[i][j] - xh * k, g[i][j]);
+                }
+        }
+        if (L.dx) {
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (on[i]) {
+                    float o[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        o[j] = a.residual_scale * g[i][j];
+                    Raw8<F32>::store(L.dx, row * H + (lane + i * lanes) * 8, o);
+                }
+        }
+        if (!a.y)
+            continue;
+        float ss[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float z = y[i].get(j) * rz;
+                S[i][j] = __builtin_fmaf(gt * g[i][j], z, S[i][j]);
+                g[i][j] *= fy[i][j];
+                ss[0] = __builtin_fmaf(g[i][j], z, ss[0]);
+            }
+        if (a.y_norm || (L.dgate && a.gate_kind == EP_GATE_TOKEN))
+            sum(ss);
+        if (L.dgate && a.gate_kind == EP_GATE_TOKEN && lane == 0)
+            store_param(L.dgate, a.gate_f32, (int)row, ss[0]);
+        if (L.dy) {
+            const float k = a.y_norm ? ss[0] * inv : 0.0f, c = rz * gt;
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (on[i]) {
+                    float o[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        o[j] = c * (g[i][j] - y[i].get(j) * rz * k);
+                    Raw8<false>::store(L.dy, row * H + (lane + i * lanes) * 8, o);
+                }
+        }
+    }
+    if (!L.part)
+        return;
+    float* part = L.part + (size_t)blockIdx.x * 2 * H;
+    if (WAVE) {
+        for (int w = 0; w < THREADS / kWave; ++w) {
+            if ((int)threadIdx.x / kWave == w)
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    if (on[i])
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const int c = (lane + i * lanes) * 8 + j;
+                            comb[c] = w ? comb[c] + P[i][j] : P[i][j];
+                            comb[H + c] = w ? comb[H + c] + S[i][j] : S[i][j];
+                        }
+            __syncthreads();
+        }
+        for (int c = threadIdx.x; c < 2 * H; c += THREADS)
+            part[c] = comb[c];
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (on[i]) {
+                Raw8<true>::store(part, (lane + i * lanes) * 8, P[i]);
+                Raw8<true>::store(part, H + (lane + i * lanes) * 8, S[i]);
+            }
+    }
+}
+
+// The workgroups' sums, added in their order: 64 columns a workgroup, four of its
+// waves share the list.
+__global__ __launch_bounds__(256) void block_norm_reduce_kernel(BlockNormBackwardLaunch L, int blocks)
+{
+    __shared__ float got[4][kWave];
+    const ep_block_norm_t& a = L.in;
+    const int H = a.width, lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+    const int which = blockIdx.y, c = blockIdx.x * kWave + lane;
+    if (which == 0 ? !L.dw : !(L.dyw || (L.dgate && a.gate_kind == EP_GATE_CHANNEL)))
+        return;
+    float v = 0.0f;
+    if (c < H)
+        for (int b = wave; b < blocks; b += 4)
+            v += L.part[((size_t)b * 2 + which) * H + c];
+    got[wave][lane] = v;
+    __syncthreads();
+    if (wave || c >= H)
+        return;
+    v = (got[0][lane] + got[1][lane]) + (got[2][lane] + got[3][lane]);
+    if (which == 0) {
+        store_param(L.dw, a.weights_f32, c, v);
+        return;
+    }
+    v *= a.y_scale;
+    const bool channel = a.gate_kind == EP_GATE_CHANNEL;
+    if (L.dyw)
+        store_param(L.dyw, a.weights_f32, c, channel ? v * load_param(a.gate, a.gate_f32, c) : v);
+    if (L.dgate && channel)
+        store_param(L.dgate, a.gate_f32, c,
+                    a.y_weight ? v * (a.weight_offset + load_param(a.y_weight, a.weights_f32, c)) : v);
+}
+
+// The team of a row and the workgroups: a wave with one or two vectors of eight a lane
+// up to a width of 1024, else a workgroup with one vector up to 2048, two up to 16384.
+struct Team {
+    bool wave;
+    int v, threads;
+    int blocks(int rows, int most) const
+    {
+        const int64_t need = wave ? ((int64_t)rows + 3) / 4 : rows;
+        return (int)(need < most ? need : most);
+    }
+};
+
+static Team team_of(int width)
+{
+    const int vecs = width / 8;
+    if (vecs <= 128)
+        return Team{true, vecs <= 64 ? 1 : 2, 256};
+    const int v = vecs <= 256 ? 1 : vecs <= 2048 ? 2 : 4;
+    return Team{false, v, ((vecs + v - 1) / v + kWave - 1) / kWave * kWave};
+}
+
+template <typename L, template <bool, int, bool, int> class K>
+static hipError_t run_team(const char* name, const Team& t, const L& args, int blocks, size_t lds, hipStream_t stream)
+{
+    debug_launch(name, dim3(blocks), dim3(t.threads), lds);
+    const bool f = args.in.x_f32;
+    void (*kernel)(L);
+    if (t.wave)
+        kernel = t.v == 1 ? (f ? K<true, 1, true, 256>::get() : K<true, 1, false, 256>::get())
+                          : (f ? K<true, 2, true, 256>::get() : K<true, 2, false, 256>::get());
+    else if (t.v == 1)
+        kernel = f ? K<false, 1, true, 256>::get() : K<false, 1, false, 256>::get();
+    else if (t.v == 2 && t.threads <= 512)
+        kernel = f ? K<false, 2, true, 512>::get() : K<false, 2, false, 512>::get();
+    else if (t.v == 2)
+        kernel = f ? K<false, 2, true, 1024>::get() : K<false, 2, false, 1024>::get();
+    else
+        kernel = f ? K<false, 4, true, 1024>::get() : K<false, 4, false, 1024>::get();
+    kernel<<<blocks, t.threads, lds, stream>>>(args);
+    return hipGetLastError();
+}
+
+template <bool WAVE, int V, bool F32, int THREADS>
+struct Forward {
+    static auto get() { return block_norm_kernel<WAVE, V, F32, THREADS>; }
+};
+template <bool WAVE, int V, bool F32, int THREADS>
+struct Backward {
+    static auto get() { return block_norm_backward_kernel<WAVE, V, F32, THREADS>; }
+};
+
+hipError_t launch_block_norm(const BlockNormLaunch& L, hipStream_t stream)
+{
+    if (L.in.num_rows == 0)
+        return hipSuccess;
+    const Team t = team_of(L.in.width);
+    return run_team<BlockNormLaunch, Forward>("block_norm", t, L, t.blocks(L.in.num_rows, kForwardBlocks), 0, stream);
+}
+
+size_t block_norm_workspace(int rows, int width)
+{
+    const int blocks = team_of(width).blocks(rows, kBackwardBlocks);
+    return ((size_t)(blocks ? blocks : 1) * 2 * width * sizeof(float) + 255) / 256 * 256;
+}
+
+hipError_t launch_block_norm_backward(const BlockNormBackwardLaunch& L, hipStream_t stream)
+{
+    const Team t = team_of(L.in.width);
+    const int blocks = t.blocks(L.in.num_rows, kBackwardBlocks);
+    if (blocks) {
+        const size_t lds = t.wave && L.part ? (size_t)2 * L.in.width * sizeof(float) : 0;
+        const hipError_t e = run_team<BlockNormBackwardLaunch, Backward>("block_norm_backward", t, L, blocks, lds, stream);
+        if (e != hipSuccess)
+            return e;
+    }
+    if (L.part) {
+        const dim3 grid((L.in.width + kWave - 1) / kWave, 2);
+        debug_launch("block_norm_reduce", grid, dim3(256), 0);
+        block_norm_reduce_kernel<<<grid, 256, 0, stream>>>(L, blocks);
+    }
+    return hipGetLastError();
+}
+
+}  // namespace moe_ep

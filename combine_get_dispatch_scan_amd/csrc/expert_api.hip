@@ -1,9 +1,13 @@
 // C entry points of the expert layer: argument checks and launches (nothing is
 // allocated and nothing waits).
-#include "api_check.h"
+#include "expert_check.h"
 #include "expert_launch.h"
 
 using moe_ep::aligned;
+using moe_ep::check_groups;
+using moe_ep::check_ptr;
+using moe_ep::check_scale_ld;
+using moe_ep::check_width;
 using moe_ep::fail;
 using moe_ep::g_err;
 using moe_ep::hip_fail;
@@ -12,47 +16,6 @@ namespace {
 
 // 1 x 128 blocks a row launch covers: 32 a workgroup of 256, and fewer than 2^32 threads.
 constexpr int64_t kMaxUnits = ((int64_t)1 << 29) - 32;
-
-bool width_ok(int w) { return w >= 128 && w <= EP_MAX_HIDDEN && w % 128 == 0; }
-
-int check_width(const char* name, int w)
-{
-    if (width_ok(w))
-        return EP_OK;
-    return fail(EP_EINVAL, "%s=%d must be a multiple of 128 in [128, %d]", name, w, EP_MAX_HIDDEN);
-}
-
-int check_groups(const int32_t* off, int G, int stride, int rows, bool optional = false)
-{
-    if (rows < 0 || rows > 0x7FFFFF00)
-        return fail(EP_EINVAL, "num_rows=%d must be in [0, 2^31 - 256]", rows);
-    if (optional && !off) {
-        if (G != 0 || stride != 0)
-            return fail(EP_EINVAL, "num_groups and group_stride must be 0 without group_offsets");
-        return EP_OK;
-    }
-    if (G < 1 || G > EP_MAX_EXPERTS)
-        return fail(EP_EINVAL, "num_groups=%d must be in [1, %d]", G, EP_MAX_EXPERTS);
-    if (stride < 0)
-        return fail(EP_EINVAL, "group_stride=%d must be >= 0", stride);
-    if (!off || !aligned(off, 4))
-        return fail(EP_EINVAL, "group_offsets must be a non-NULL 4-byte aligned device pointer");
-    return EP_OK;
-}
-
-int check_ptr(const char* name, const void* p, size_t a)
-{
-    if (p && aligned(p, a))
-        return EP_OK;
-    return fail(EP_EINVAL, "%s must be a non-NULL %zu-byte aligned device pointer", name, a);
-}
-
-int check_scale_ld(int ld, int rows)
-{
-    if (ld == 0 || (ld >= rows && ld % 4 == 0))
-        return EP_OK;
-    return fail(EP_EINVAL, "scale_ld=%d must be 0, or >= num_rows=%d and a multiple of 4", ld, rows);
-}
 
 int check_units(int rows, int width)
 {
@@ -86,13 +49,6 @@ int check_gate(const void* logits, int bf16, const GateDims& d, int normalize)
 }
 
 }  // namespace
-
-#define EP_TRY(call)          \
-    do {                      \
-        const int rc_ = call; \
-        if (rc_)              \
-            return rc_;       \
-    } while (0)
 
 extern "C" {
 

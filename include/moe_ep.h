@@ -122,7 +122,7 @@ typedef struct ep_handle {
 
 /* Library version, major*10000 + minor*100 + patch.  EP_VERSION is the
  * version of this header; ep_version() that of the loaded library. */
-#define EP_VERSION 10300
+#define EP_VERSION 10400
 int ep_version(void);
 
 /* Message describing the last error returned on this thread ("" if none). */
@@ -631,6 +631,124 @@ int ep_swiglu_fp8_backward(const void* grad_a, const void* ckpt, const float* ck
                            const int32_t* group_offsets, int num_groups, int group_stride,
                            int num_rows, int scale_ld, void* grad_h, void* codes, float* scales,
                            hipStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Around the expert layer: the norms before and after a block with its gate and
+ * residual scales, and expert weights in 4 bits.
+ * ------------------------------------------------------------------------- */
+
+#define EP_GATE_NONE    0
+#define EP_GATE_TOKEN   1   /* gate [num_rows]: one factor a row         */
+#define EP_GATE_CHANNEL 2   /* gate [width]: one factor a channel        */
+
+/*
+ * What a block norm is given, forward and backward.  With y, a block's output
+ * (combine's), for every row
+ *   z  = y / sqrt(mean(y^2) + eps)                   (y_norm, else z = y)
+ *   n  = z * (weight_offset + y_weight)              (y_weight, else n = z)
+ *   x' = residual_scale * x + y_scale * gate * n     (without y: x' = x)
+ *   h  = x' / sqrt(mean(x'^2) + eps) * (weight_offset + weight)   (norm;
+ *        without weight: no factor)
+ * in fp32, h from the x' that was not rounded yet.  The mean squares must stay
+ * in fp32's range (values below 2^63); eps keeps rows of zeros finite.
+ *
+ *   x, x_f32       device bf16 or (x_f32) fp32, row r from x + r*x_ld
+ *   y              device bf16, row r from y + r*y_ld, or NULL
+ *   x_ld, y_ld     elements between rows, >= width, multiples of 8
+ *   width          multiple of 8 in [8, EP_MAX_HIDDEN]
+ *   norm, y_norm   0 or 1; y_norm, y_weight and a gate need y; without y,
+ *                  residual_scale is 1 and norm 1; weight needs norm
+ *   weight, y_weight, weights_f32   device bf16 or (weights_f32) fp32 [width], or NULL
+ *   gate, gate_kind, gate_f32       device bf16 or (gate_f32) fp32, EP_GATE_*
+ *   eps            in [2^-100, 2^100]
+ * x, y, weight, y_weight and a channel's gate are 16-byte aligned.
+ */
+typedef struct ep_block_norm_t {
+    const void* x;
+    const void* y;
+    const void* weight;
+    const void* y_weight;
+    const void* gate;
+    int64_t x_ld;
+    int64_t y_ld;
+    int32_t num_rows;
+    int32_t width;
+    int32_t x_f32;
+    int32_t norm;
+    int32_t y_norm;
+    int32_t weights_f32;
+    int32_t gate_kind;
+    int32_t gate_f32;
+    float residual_scale;
+    float y_scale;
+    float eps;
+    float weight_offset;
+} ep_block_norm_t;
+
+/*
+ * Forward.
+ *   x_out          x' of x's type, dense [num_rows][width]; with y.  It may be x
+ *                  itself where x is dense.  NULL: not written
+ *   h              device bf16 [num_rows][width], with norm.  NULL: not written
+ *   codes, scales  NULL, or h (from its fp32 values) as FP8 rows with dispatch's
+ *                  arithmetic, scales [num_rows][width/128]: what ep_dispatch_ex
+ *                  takes as x, x_scales.  width a multiple of 128, with norm
+ * One output is given.  Errors: EP_EINVAL, EP_EHIP.
+ */
+int ep_block_norm(const ep_block_norm_t* args, void* x_out, void* h, void* codes, float* scales,
+                  hipStream_t stream);
+
+/*
+ * Backward, from the same arguments (x and y as the forward call read them) and
+ * the gradients of x' and h:
+ *   grad_x         gradient of x', of x's type, dense, or NULL (zero)
+ *   grad_h         gradient of h, bf16, dense, or NULL (zero); with norm
+ *   out_x, out_y   gradients of x (its type) and y (bf16), dense.  out_x may be grad_x
+ *   out_weight, out_y_weight   fp32 or bf16 like the weights, [width]
+ *   out_gate       like the gate, [num_rows] or [width]
+ * NULL outputs are not written; one is given.  Sums over rows are taken in an
+ * order fixed by the sizes: results repeat bit for bit.
+ *   ws             ep_block_norm_workspace_bytes(num_rows, width) bytes, 256-byte
+ *                  aligned, where out_weight, out_y_weight or a channel's out_gate is
+ *                  given (else NULL); free again once the call's work has run
+ * Errors: EP_EINVAL, EP_EHIP.
+ */
+size_t ep_block_norm_workspace_bytes(int num_rows, int width);
+int ep_block_norm_backward(const ep_block_norm_t* args, const void* grad_x, const void* grad_h,
+                           void* out_x, void* out_y, void* out_weight, void* out_y_weight,
+                           void* out_gate, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/*
+ * Weights in 4 bits: E2M1 codes (0, 1/2, 1, 3/2, 2, 3, 4, 6 and their negatives)
+ * and one E8M0 scale (a power of two, its exponent + 127 in a byte) for 32
+ * weights along k.  The scale is the smallest power of two s >= 2^-127 with
+ * max |w| < 7 s, so no weight is cut by more than half a step; codes are w / s
+ * rounded to nearest, ties to the even code.  A group that holds a NaN or an
+ * infinity gets the scale 0xFF (NaN).
+ *   w       [G][N][K] bf16 or (w_f32) fp32; n, k multiples of 128
+ *   codes   device uint8 [G][N][K/2], an even k in the low half
+ *   scales  device uint8 [G][N][K/32]
+ * ep_dequantize_weights_fp4 writes code * scale as bf16 or (out_f32) fp32 [G][N][K],
+ * exactly (2^128 and more, which a weight above 7/8 of that rounds to, is infinite).
+ * All arrays 16-byte aligned, scales 4-byte.  Errors: EP_EINVAL, EP_EHIP.
+ */
+int ep_quantize_weights_fp4(const void* w, int w_f32, int num_groups, int n, int k, void* codes,
+                            void* scales, hipStream_t stream);
+int ep_dequantize_weights_fp4(const void* codes, const void* scales, int num_groups, int n, int k,
+                              void* out, int out_f32, hipStream_t stream);
+
+/*
+ * Grouped product of FP8 rows with 4-bit weights: ep_grouped_gemm_fp8 with
+ *   out[r][n] = bf16_rne( sum over blocks b of 128 k of x_scales[r][b]
+ *                         * sum over k in b of x[r][k] * code[g][n][k] * scale[g][n][k/32] )
+ * The inner sums (exact products, the powers of two applied to sums of 32) and
+ * the outer ones are fp32.  w, w_scales: as ep_quantize_weights_fp4 writes them;
+ * the other arguments are ep_grouped_gemm_fp8's.  Errors: EP_EINVAL, EP_EHIP.
+ */
+int ep_grouped_gemm_fp4(const void* x, const float* x_scales, int scale_ld, const void* w,
+                        const void* w_scales, const int32_t* group_offsets, int num_groups,
+                        int group_stride, int num_rows, int n, int k, int expected_rows, void* out,
+                        hipStream_t stream);
 
 #ifdef __cplusplus
 }
