@@ -7,12 +7,10 @@
 // operand: a lane then holds four neighbouring columns of one row and needs one
 // scale for them.
 #include "expert_launch.h"
-#include "mfma.h"
+#include "gemm_tile.h"
 #include "moe_ep.h"
 
 namespace moe_ep {
-
-constexpr int kXcds = 8, kCus = 256;
 
 // Skinny tiles, for few rows a group: a workgroup's four waves split the K
 // blocks of a 16*RT x 16*CT tile between them (operands straight from memory to
@@ -118,10 +116,7 @@ __global__ __launch_bounds__(256) void gemm_skinny_kernel(GemmLaunch a)
 // Large tiles: 256 rows x 256 columns by eight waves, each 64 rows x 128
 // columns (one scale block of the weights).  One K block of both operands
 // (2 x 32 KB and the rows' scales) is computed from LDS while the next one is
-// copied in behind it.  LDS rows are the 128 bytes of a K block; a row's 16-byte
-// chunks are permuted by its number, which the copy does for free (it chooses
-// which global chunk lands where), so that eight rows read at the same chunk
-// hit all banks once.
+// copied in behind it.  LDS rows are the 128 bytes of a K block, their chunks permuted.
 //
 // 65536 rows in 32 groups, N = 4096, K = 7168: 1838-1899 us over five inputs on one card,
 // 1949 on another, 1.97-2.09 PFLOP/s, where a library product of E4M3 matrices with one
@@ -131,9 +126,6 @@ __global__ __launch_bounds__(256) void gemm_skinny_kernel(GemmLaunch a)
 // 1442 us (no copies after the first two blocks): the two do not overlap fully.  Forms
 // with a stream of stages across tiles, copies one and a half stages ahead, or pinned
 // fetches into L2 came out within 3% or slower.
-constexpr int kTile = 256;
-constexpr int kStage = kTile * kQBlock;
-
 // Where a tile's operands come from, and this lane's offsets.  Wave w copies rows
 // 8 * (8 * i + w) .. + 7 of both operands.
 struct TileSource {
@@ -155,46 +147,6 @@ __device__ __forceinline__ void copy_stage(const TileSource& t, int kb, int wave
     }
 }
 
-// The rows' scales of blocks kb .. kb + 3, by waves 0-3, 64 rows each.  In row-major
-// scales every row is a cache line of its own, so the four are fetched together:
-// one by one they were a third of all requests a tile makes (1950 against 1865 us
-// at 65536 x 4096 x 7168).
-__device__ __forceinline__ void copy_scales(const TileSource& t, int kb, int KB, int wave, float* ls)
-{
-    if (wave >= 4)
-        return;
-    if (t.four) {
-        load_to_lds16(t.xs + (t.so + kb), ls + wave * 256);            // [row][block]
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {                                  // [block][row]
-            const int k = min(kb + i, KB - 1);
-            load_to_lds4(t.xs + (t.so + (t.sld ? (size_t)k * t.sld : k)), ls + i * kTile + wave * 64);
-        }
-    }
-}
-
-// The permutation of row r's chunks, w's and x's: the eight rows that lanes read
-// together (see read_w, read_x) have eight different ones.
-__device__ __forceinline__ int place_w(int r) { return (r & 3) | ((r >> 1) & 4); }
-__device__ __forceinline__ int place_x(int r) { return r & 7; }
-
-__device__ __forceinline__ i32x8 read_fragment(const uint8_t* row, int place, int lane)
-{
-    const int c = lane >> 4;
-    const u32x4 lo = *reinterpret_cast<const u32x4*>(row + ((c ^ place) << 4));
-    const u32x4 hi = *reinterpret_cast<const u32x4*>(row + (((c + 4) ^ place) << 4));
-    return join(lo, hi);
-}
-
-__device__ __forceinline__ i32x8 read_x(const uint8_t* lds, int row0, int r, int lane)
-{
-    const int row = row0 + 16 * r + (lane & 15);
-    return read_fragment(lds + row * kQBlock, place_x(row), lane);
-}
-
-// Column tiles 2i and 2i + 1 take every other four of 32 columns, so that a lane's
-// results of both are eight neighbouring columns (one 16-byte store).
 __device__ __forceinline__ i32x8 read_w(const uint8_t* lds, int col0, int c, int lane)
 {
     const int row = col0 + 32 * (c >> 1) + ((lane & 12) << 1) + (lane & 3) + 4 * (c & 1);
