@@ -22,104 +22,114 @@ __device__ __forceinline__ f32x4 mfma_fp4_fp8(const u32x4& a, const i32x8& b, ui
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, b, zero, 4, 0, 0, (int)s, 0, 0x7F7F7F7F);
 }
 
-// Skinny tiles: a workgroup's four waves split the K blocks of a 16*RT x 16*CT tile
-// between them (operands straight from memory to registers, each weight byte read by
-// one lane) and add up through LDS.
-template <int RT, int CT>
-__global__ __launch_bounds__(256) void gemm_fp4_skinny_kernel(GemmFp4Launch a)
+// Streamed columns, for few rows: a wave keeps B blocks of 16 rows in registers and runs
+// over columns, 16 at a time, so that nothing but weights (B * 64 neighbouring bytes of a
+// column) and their scales is read in the loop, one step ahead.  The workgroup's waves
+// share K; every 64 columns their sums meet in LDS.
+constexpr int kStreamSteps = 4, kStreamCols = 16 * kStreamSteps, kStreamWaves = 8;
+
+template <int B, bool FOUR>
+__global__ __launch_bounds__(kStreamWaves* kWave) void gemm_fp4_stream_kernel(GemmFp4Launch a)
 {
-    constexpr int kRows = 16 * RT, kCols = 16 * CT, kStep = 2;
-    extern __shared__ int prefix[];
-    __shared__ f32x4 part[4][RT][CT][kWave];
-    const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave, q = lane >> 4;
-    const int N = a.N, K = a.K, KB = K / kQBlock, NT = N / kCols;
-    tile_prefix<kRows>(a.groups, prefix);
+    extern __shared__ __align__(16) char lds[];       // [2][steps][waves][64] sums of four, then the prefix
+    const int tid = threadIdx.x, lane = tid % kWave, wave = __builtin_amdgcn_readfirstlane(tid / kWave), q = lane >> 4;
+    const int waves = blockDim.x / kWave;
+    f32x4* part = reinterpret_cast<f32x4*>(lds);
+    int* prefix = reinterpret_cast<int*>(lds + (size_t)2 * kStreamSteps * waves * kWave * sizeof(f32x4));
+    const int N = a.N, K = a.K, KB = K / kQBlock, NB = N / kStreamCols;
+    tile_prefix<16>(a.groups, prefix);
     __syncthreads();
-    const int64_t total = (int64_t)prefix[a.groups.num] * NT;
-    const int64_t per = (total + kXcds - 1) / kXcds;
-    const int xcd = blockIdx.x % kXcds;
-    for (int64_t i = blockIdx.x / kXcds; i < per; i += gridDim.x / kXcds) {
-        const int64_t t = xcd * per + i;
-        if (t >= total)
-            break;
-        const int g = find_group(prefix, a.groups.num, t, NT);
+    const int64_t total = (int64_t)prefix[a.groups.num] * NB;
+    const int64_t first = total * blockIdx.x / gridDim.x, last = total * (blockIdx.x + 1) / gridDim.x;
+    const int kb0 = wave * B;
+    const int64_t sstep = a.x_scale_ld ? a.x_scale_ld : 1;
+    i32x8 x[B];
+    float sx[B];
+    u32x4 w[2][B];
+    uint32_t ws[2][B];
+    int turn = 0;
+    int64_t t = first;
+    while (t < last) {
+        const int g = __builtin_amdgcn_readfirstlane(find_group(prefix, a.groups.num, t, NB));
         int begin, end;
         group_bounds(a.groups, g, begin, end);
-        const int mt = prefix[g + 1] - prefix[g];
-        const int64_t local = t - (int64_t)prefix[g] * NT;
-        const int m0 = begin + (int)(local % mt) * kRows, n0 = (int)(local / mt) * kCols;
-        f32x4 acc[RT][CT];
-        const uint8_t* xp[RT];
-        const float* sp[RT];
-        const int64_t sstep = a.x_scale_ld ? a.x_scale_ld : 1;
+        const int64_t local = t - (int64_t)prefix[g] * NB;
+        const int m0 = begin + (int)(local / NB) * 16;
+        int n0 = (int)(local % NB) * kStreamCols;
+        const int64_t stop = min(last, t + NB - local % NB);         // items of the same rows
+        const int row = min(m0 + (lane & 15), end - 1);              // rows past the group: its last one, not stored
+        const uint8_t* xp = a.x + (size_t)row * K + q * 16;
+        const float* sp = a.x_scales + scale_at(row, 0, KB, a.x_scale_ld);
 #pragma unroll
-        for (int r = 0; r < RT; ++r) {
-            int row = m0 + 16 * r + (lane & 15);
-            row = row < end ? row : end - 1;           // rows past the group: any of its rows, not stored
-            xp[r] = a.x + (size_t)row * K + q * 16;
-            sp[r] = a.x_scales + scale_at(row, 0, KB, a.x_scale_ld);
-#pragma unroll
-            for (int c = 0; c < CT; ++c)
-                acc[r][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int u = 0; u < B; ++u) {
+            const int kb = min(kb0 + u, KB - 1);
+            x[u] = join(load16_hint<false>(xp + (size_t)kb * kQBlock), load16_hint<false>(xp + (size_t)kb * kQBlock + 64));
+            sx[u] = sp[kb * sstep];
         }
         const size_t col = (size_t)g * N + n0 + (lane & 15);
         const uint8_t* wp = a.w + col * (K / 2) + q * 16;
-        const uint8_t* wsp = a.w_scales + col * (K / 32) + q;
-        // a wave takes two neighbouring blocks at a time: 128 bytes of a column
-        for (int kb0 = kStep * wave; kb0 < KB; kb0 += 4 * kStep) {
-            u32x4 w[kStep][CT], x[kStep][RT][2];
-            uint32_t ws[kStep][CT];
-            float s[kStep][RT];
+        const uint32_t* wsp = reinterpret_cast<const uint32_t*>(a.w_scales) + col * KB;
+        const auto load = [&](u32x4 (&w)[B], uint32_t (&ws)[B]) {
 #pragma unroll
-            for (int u = 0; u < kStep; ++u) {
-                const int kb = kb0 + u < KB ? kb0 + u : KB - 1;
+            for (int u = 0; u < B; ++u)
+                w[u] = load16_hint<false>(wp + (size_t)min(kb0 + u, KB - 1) * 64);
+            if constexpr (FOUR && B >= 4) {
 #pragma unroll
-                for (int c = 0; c < CT; ++c) {
-                    w[u][c] = load16_hint<false>(wp + (size_t)16 * c * (K / 2) + (size_t)kb * 64);
-                    ws[u][c] = wsp[(size_t)16 * c * (K / 32) + (size_t)kb * 4];
+                for (int u = 0; u < B; u += 4) {
+                    const u32x4 v = load16_hint<false>(wsp + min(kb0 + u, KB - 4));
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        ws[u + j] = v[j];
                 }
+            } else {
 #pragma unroll
-                for (int r = 0; r < RT; ++r) {
-                    const uint8_t* p = xp[r] + (size_t)kb * kQBlock;
-                    x[u][r][0] = load16_hint<false>(p);
-                    x[u][r][1] = load16_hint<false>(p + 64);
-                    s[u][r] = sp[r][kb * sstep];
-                }
+                for (int u = 0; u < B; ++u)
+                    ws[u] = wsp[min(kb0 + u, KB - 1)];
             }
+            wp += (size_t)16 * (K / 2);
+            wsp += (size_t)16 * KB;
+        };
+        const auto compute = [&](const u32x4 (&w)[B], const uint32_t (&ws)[B], int step) {
+            f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-            for (int u = 0; u < kStep; ++u) {
+            for (int u = 0; u < B; ++u) {
                 if (kb0 + u >= KB)
                     break;
+                const f32x4 d = mfma_fp4_fp8(w[u], x[u], ws[u] >> (8 * q));
 #pragma unroll
-                for (int r = 0; r < RT; ++r)
-#pragma unroll
-                    for (int c = 0; c < CT; ++c) {
-                        const f32x4 d = mfma_fp4_fp8(w[u][c], join(x[u][r][0], x[u][r][1]), ws[u][c]);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            acc[r][c][j] = __builtin_fmaf(d[j], s[u][r], acc[r][c][j]);
-                    }
+                for (int j = 0; j < 4; ++j)
+                    acc[j] = __builtin_fmaf(d[j], sx[u], acc[j]);
             }
+            part[((turn * kStreamSteps + step) * waves + wave) * kWave + lane] = acc;
+        };
+        load(w[0], ws[0]);
+        for (; t < stop; ++t) {
+            load(w[1], ws[1]);
+            compute(w[0], ws[0], 0);
+            load(w[0], ws[0]);
+            compute(w[1], ws[1], 1);
+            load(w[1], ws[1]);
+            compute(w[0], ws[0], 2);
+            if (t + 1 < stop)
+                load(w[0], ws[0]);
+            compute(w[1], ws[1], 3);
+            // LDS only: the loads on their way need not have come
+            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+            __builtin_amdgcn_s_barrier();
+            __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+            for (int i = wave; i < kStreamSteps; i += waves) {
+                const f32x4* p = part + (size_t)(turn * kStreamSteps + i) * waves * kWave + lane;
+                f32x4 v = p[0];
+                for (int o = 1; o < waves; ++o)
+                    v += p[o * kWave];
+                if (m0 + (lane & 15) < end)
+                    *reinterpret_cast<uint2*>(a.out + (size_t)row * N + n0 + 16 * i + 4 * q) =
+                        uint2{pack2_bf16(v[0], v[1]), pack2_bf16(v[2], v[3])};
+            }
+            // the sums of this turn are written again two barriers on
+            turn ^= 1;
+            n0 += kStreamCols;
         }
-#pragma unroll
-        for (int r = 0; r < RT; ++r)
-#pragma unroll
-            for (int c = 0; c < CT; ++c)
-                part[wave][r][c][lane] = acc[r][c];
-        __syncthreads();
-        // wave w finishes tiles w, w + 4, ...: the four partial sums in wave order
-        for (int i = wave; i < RT * CT; i += 4) {
-            const int r = i / CT, c = i % CT;
-            f32x4 v = part[0][r][c][lane];
-#pragma unroll
-            for (int w = 1; w < 4; ++w)
-                v += part[w][r][c][lane];
-            const int row = m0 + 16 * r + (lane & 15);
-            if (row < end)
-                *reinterpret_cast<uint2*>(a.out + (size_t)row * N + n0 + 16 * c + 4 * q) =
-                    uint2{pack2_bf16(v[0], v[1]), pack2_bf16(v[2], v[3])};
-        }
-        __syncthreads();
     }
 }
 
@@ -128,6 +138,14 @@ __global__ __launch_bounds__(256) void gemm_fp4_skinny_kernel(GemmFp4Launch a)
 // block; of w two blocks at a time (128 bytes of a column, a whole cache line), half of
 // the columns with each of the two blocks before.  The scales of four blocks are fetched
 // together: 16 bytes of a row of x, 16 of a column of w.
+//
+// 16384 rows in 32 groups, 4096 x 7168: 527 us, 1.82 PFLOP/s; 65536 rows 1764 us, 2.2 of
+// the 3.5 PFLOP/s that these instructions with the scaled sums reach from registers.  The
+// clock falls to 1.8 GHz, and the copies through L2 (1.2 ms without products) overlap the
+// products (1.3 ms without copies) in part.  Forms that came out slower there: three
+// buffers with copies two blocks ahead (1982), the same with the two waves of a SIMD
+// taking turns between LDS and products (1860), touching lines six blocks ahead (2400),
+// two workgroups a CU with 128 x 256 tiles (1995).
 struct TileFp4Source {
     const uint8_t* x;             // first row of the tile
     const uint8_t* w;
@@ -233,8 +251,11 @@ __global__ __launch_bounds__(512, 2) void gemm_fp4_tile_kernel(GemmFp4Launch a)
         group_bounds(a.groups, g, begin, end);
         const int mt = prefix[g + 1] - prefix[g];
         const int local = (int)(t - (int64_t)prefix[g] * NT);
-        const int m0 = __builtin_amdgcn_readfirstlane(begin + (local % mt) * kTile);
-        const int n0 = __builtin_amdgcn_readfirstlane((local / mt) * kTile);
+        // bands of four row tiles, columns within a band: what the CUs of an XCD read at a time is smallest
+        // where a tile's rows are twice its columns' bytes (1764 us against 1802 at 65536 x 4096 x 7168)
+        const int band = local / (4 * NT), hb = min(4, mt - 4 * band), lb = local - band * 4 * NT;
+        const int m0 = __builtin_amdgcn_readfirstlane(begin + (4 * band + lb % hb) * kTile);
+        const int n0 = __builtin_amdgcn_readfirstlane((lb / hb) * kTile);
         TileFp4Source src;
         src.x = a.x + (size_t)m0 * K;
         src.w = a.w + ((size_t)g * N + n0) * (K / 2);
@@ -329,32 +350,255 @@ __global__ __launch_bounds__(512, 2) void gemm_fp4_tile_kernel(GemmFp4Launch a)
     }
 }
 
-template <int RT, int CT>
-static void skinny_run(const GemmFp4Launch& L, hipStream_t stream)
+// Small tiles, 64 rows x 128 columns by four waves of 32 x 64 each, two K blocks at a time
+// (256 bytes of a row, 128 of a column) from LDS while the next two are copied in behind
+// them; two workgroups a CU, so that one computes while the other waits.  256 rows in 32
+// groups, 4096 x 7168: 92 us, 5.5 TB/s (HBM); 4096 rows in 64 groups with zipf popularity,
+// 2816 x 2048: 66 us (two rounds of tiles, 0.71 PFLOP/s).
+constexpr int kSmallRows = 64, kSmallCols = 128;
+constexpr int kPairStage = 64 * 2 * kQBlock;      // x's and w's alike
+
+template <bool FOUR>
+__global__ __launch_bounds__(256, 2) void gemm_fp4_small_kernel(GemmFp4Launch a)
 {
-    const size_t lds = (size_t)(L.groups.num + 1) * 4;
-    const dim3 grid(kCus * 4);
-    debug_launch("grouped_gemm_fp4_skinny", grid, dim3(256), lds);
-    gemm_fp4_skinny_kernel<RT, CT><<<grid, 256, lds, stream>>>(L);
+    __shared__ __align__(1024) uint8_t lx0[kPairStage], lx1[kPairStage], lw0[kPairStage], lw1[kPairStage];
+    __shared__ __align__(16) float ls[2][4 * kSmallRows];
+    __shared__ __align__(16) uint8_t lws[2][16 * kSmallCols];
+    extern __shared__ int prefix[];
+    const int tid = threadIdx.x, lane = tid % kWave, wave = __builtin_amdgcn_readfirstlane(tid / kWave), q = lane >> 4;
+    const int N = a.N, K = a.K, KB = K / kQBlock, pairs = (KB + 1) / 2, NT = N / kSmallCols;
+    tile_prefix<kSmallRows>(a.groups, prefix);
+    __syncthreads();
+    const int64_t total = (int64_t)prefix[a.groups.num] * NT;
+    const int row0 = (wave >> 1) * 32, col0 = (wave & 1) * 64;
+    const int xrow = row0 + (lane & 15), col = column_of(col0, 0, lane);
+    const int xbase = xrow * 2 * kQBlock + ((q ^ (lane & 7)) << 4);
+    const int wbase = col * kQBlock + ((q ^ place_w(col)) << 4);
+    const int wsbase = col * (FOUR ? 16 : 4) + q;
+    const bool four = !a.x_scale_ld && KB % 4 == 0 && reinterpret_cast<uintptr_t>(a.x_scales) % 16 == 0;
+    const int64_t per = (total + kXcds - 1) / kXcds;
+    const int xcd = blockIdx.x % kXcds;
+    for (int64_t i = blockIdx.x / kXcds; i < per; i += gridDim.x / kXcds) {
+        const int64_t t = xcd * per + i;
+        if (t >= total)
+            break;
+        const int g = __builtin_amdgcn_readfirstlane(find_group(prefix, a.groups.num, t, NT));
+        int begin, end;
+        group_bounds(a.groups, g, begin, end);
+        const int mt = prefix[g + 1] - prefix[g];
+        const int64_t local = t - (int64_t)prefix[g] * NT;
+        const int m0 = __builtin_amdgcn_readfirstlane(begin + (int)(local % mt) * kSmallRows);
+        const int n0 = __builtin_amdgcn_readfirstlane((int)(local / mt) * kSmallCols);
+        const int last_row = end - 1 - m0;                        // rows past the end: the last one again
+        const uint8_t* xp = a.x + (size_t)m0 * K;
+        const uint8_t* wp = a.w + ((size_t)g * N + n0) * (K / 2);
+        const uint8_t* wsp = a.w_scales + ((size_t)g * N + n0) * (K / 32);
+        const float* xsp = a.x_scales + scale_at(m0, 0, KB, a.x_scale_ld);
+        uint32_t xo[4], wo[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int r = (4 * j + wave) * 4 + (lane >> 4);       // 256 bytes of four rows a copy
+            xo[j] = (uint32_t)min(r, last_row) * K + ((lane & 15) ^ (r & 7)) * 16;
+            const int c = (4 * j + wave) * 8 + (lane >> 3);       // 128 bytes of eight columns
+            wo[j] = (uint32_t)c * (K / 2) + ((lane & 7) ^ place_w(c)) * 16;
+        }
+        // an odd number of blocks ends with half a pair: its first half stands in for the second (the permutations'
+        // high bits: none of x's, bit 0 of the wave of w's)
+        const int xtail = (KB & 1) && (lane & 8) ? kQBlock : 0;
+        const int wtail = (KB & 1) && (((lane >> 2) ^ wave) & 1) ? kQBlock / 2 : 0;
+        const auto copy = [&](int p, uint8_t* lx, uint8_t* lw) {
+            const bool end = p == pairs - 1;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                load_to_lds16(wp + (wo[j] + p * kQBlock - (end ? wtail : 0)), lw + (4 * j + wave) * 1024);
+                load_to_lds16(xp + (xo[j] + p * 2 * kQBlock - (end ? xtail : 0)), lx + (4 * j + wave) * 1024);
+            }
+        };
+        // the scales of blocks kb .. kb + 3: the rows' by wave 0, the columns' by waves 1 and 2
+        const auto copy_scales_of = [&](int kb, float* s, uint8_t* sw) {
+            if (wave == 0) {
+                const uint32_t row = min(lane, last_row), so = a.x_scale_ld ? row : row * KB;
+                if (four) {
+                    load_to_lds16(xsp + (so + kb), s);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int k = min(kb + j, KB - 1);
+                        load_to_lds4(xsp + (so + (a.x_scale_ld ? (size_t)k * a.x_scale_ld : k)), s + j * kSmallRows);
+                    }
+                }
+            } else if (wave < 3) {
+                const uint32_t o = ((wave - 1) * 64 + lane) * (uint32_t)(K / 32);
+                if (FOUR) {
+                    load_to_lds16(wsp + (o + kb * 4), sw + (wave - 1) * 1024);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        load_to_lds4(wsp + (o + min(kb + j, KB - 1) * 4), sw + j * (4 * kSmallCols) + (wave - 1) * 256);
+                }
+            }
+        };
+        const bool on = row0 <= last_row;
+        f32x4 acc[2][4];
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                acc[r][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        copy(0, lx0, lw0);
+        copy_scales_of(0, ls[0], lws[0]);
+        __syncthreads();
+        // pair p from lx, lw, while pair p + 1 goes to nx, nw.  The scales are read first: the compiler would wait for
+        // the copies of later ones
+        const auto stage = [&](int p, const uint8_t* lx, const uint8_t* lw, uint8_t* nx, uint8_t* nw) {
+            float s[2][2];
+            uint32_t ws[2][4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int kb = 2 * p + h, b = kb & 3;
+                const float* f = ls[(kb >> 2) & 1] + (four ? xrow * 4 + b : b * kSmallRows + xrow);
+                const uint8_t* u = lws[(kb >> 2) & 1] + wsbase + b * (FOUR ? 4 : 4 * kSmallCols);
+#pragma unroll
+                for (int r = 0; r < 2; ++r)
+                    s[h][r] = f[(four ? 64 : 16) * r];
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    ws[h][c] = u[(32 * (c >> 1) + 4 * (c & 1)) * (FOUR ? 16 : 4)];
+            }
+            if (p + 1 < pairs) {
+                copy(p + 1, nx, nw);
+                if ((p & 1) == 1)
+                    copy_scales_of(2 * p + 2, ls[((p + 1) >> 1) & 1], lws[((p + 1) >> 1) & 1]);
+            }
+            if (on) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    if (2 * p + h >= KB)
+                        break;
+                    i32x8 x[2];
+                    u32x4 w[4];
+#pragma unroll
+                    for (int r = 0; r < 2; ++r)
+                        x[r] = join(*reinterpret_cast<const u32x4*>(lx + xbase + (16 * r * 2 + h) * kQBlock),
+                                    *reinterpret_cast<const u32x4*>(lx + (xbase ^ 64) + (16 * r * 2 + h) * kQBlock));
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        w[c] = *reinterpret_cast<const u32x4*>(lw + (wbase ^ (64 * h)) + (32 * (c >> 1) + 4 * (c & 1)) * kQBlock);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) {
+                            const f32x4 d = mfma_fp4_fp8(w[c], x[r], ws[h][c]);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                acc[r][c][j] = __builtin_fmaf(d[j], s[h][r], acc[r][c][j]);
+                        }
+                }
+            }
+            __syncthreads();
+        };
+        for (int p = 0; p < pairs; p += 2) {
+            stage(p, lx0, lw0, lx1, lw1);
+            if (p + 1 < pairs)
+                stage(p + 1, lx1, lw1, lx0, lw0);
+        }
+        if (on) {
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const int row = xrow + 16 * r;
+                if (row > last_row)
+                    continue;
+                uint16_t* o = a.out + (size_t)(m0 + row) * N + n0 + col0 + 8 * q;
+#pragma unroll
+                for (int c = 0; c < 4; c += 2)
+                    store16_hint<false>(o + 16 * c, u32x4{pack2_bf16(acc[r][c][0], acc[r][c][1]),
+                                                          pack2_bf16(acc[r][c][2], acc[r][c][3]),
+                                                          pack2_bf16(acc[r][c + 1][0], acc[r][c + 1][1]),
+                                                          pack2_bf16(acc[r][c + 1][2], acc[r][c + 1][3])});
+            }
+        }
+    }
 }
 
+// Row tiles of `tile` rows that the groups can have at most.
+static int64_t most_tiles(const Groups& g, int tile)
+{
+    return (g.rows < g.num ? g.rows : g.num) + (int64_t)g.rows / tile;
+}
+
+template <int B>
+static void stream_run(const GemmFp4Launch& L, hipStream_t stream)
+{
+    const int KB = L.K / kQBlock, waves = (KB + B - 1) / B;
+    const size_t lds = (size_t)2 * kStreamSteps * waves * kWave * sizeof(f32x4) + (size_t)(L.groups.num + 1) * 4;
+    const int64_t items = most_tiles(L.groups, 16) * (L.N / kStreamCols), room = kCus * (kStreamWaves / waves);
+    const dim3 blocks((unsigned)(items < room ? items : room));
+    debug_launch("grouped_gemm_fp4_stream", blocks, dim3(waves * kWave), lds);
+    const bool four = KB % 4 == 0 && reinterpret_cast<uintptr_t>(L.w_scales) % 16 == 0;
+    auto* kernel = four ? gemm_fp4_stream_kernel<B, true> : gemm_fp4_stream_kernel<B, false>;
+    kernel<<<blocks, waves * kWave, lds, stream>>>(L);
+}
+
+static void small_run(const GemmFp4Launch& L, hipStream_t stream)
+{
+    const size_t lds = (size_t)(L.groups.num + 1) * 4;
+    const int64_t tiles = (most_tiles(L.groups, kSmallRows) * (L.N / kSmallCols) + kXcds - 1) / kXcds * kXcds;
+    const dim3 blocks((unsigned)(tiles < 2 * kCus ? tiles : 2 * kCus));
+    debug_launch("grouped_gemm_fp4_small", blocks, dim3(256), lds);
+    const bool four = L.K % 512 == 0 && reinterpret_cast<uintptr_t>(L.w_scales) % 16 == 0;
+    auto* kernel = four ? gemm_fp4_small_kernel<true> : gemm_fp4_small_kernel<false>;
+    kernel<<<blocks, 256, lds, stream>>>(L);
+}
+
+static void tile_run(const GemmFp4Launch& L, hipStream_t stream)
+{
+    debug_launch("grouped_gemm_fp4_tile", dim3(kCus), dim3(512), 0);
+    const bool four = L.K % 512 == 0 && reinterpret_cast<uintptr_t>(L.w_scales) % 16 == 0;
+    auto* kernel = four ? gemm_fp4_tile_kernel<true> : gemm_fp4_tile_kernel<false>;
+    kernel<<<kCus, 512, 0, stream>>>(L);
+}
+
+// The form by the typical rows m of a group.  32 groups, N = 4096, K = 7168 (499 MB of
+// weights and scales; 98 us at the rate of a large copy), in us, rows falling evenly:
+//   rows in all     8     64    128    256    512   1024   2048   4096   8192  16384
+//   streamed       26     82     92     98    130    211
+//   small          34     85     90     92     95    104    151    217    366    710
+//   large          71    143    146    146    146    148    160    195    333    527
+// (8 rows: eight groups of one.)  Beyond such full cards it is how many tiles there are
+// that counts: a form's time is that of its rounds over the card, and a round costs
+// nearly the same however few tiles are in it.  So the form is the one with the least of
+//   streamed  8.0 + rounds * (2.25 + 0.2 KB)       KB: blocks of K
+//   small     6.5 + KB * max(0.8, tiles / 700)
+//   large     6.5 + rounds * 1.65 KB               us
+// which was fitted to 259 shapes (1 to 64 groups, m = 1 to 1024, N and K up to 8192, even,
+// equal and zipf rows).  There this choice takes 2.0 % longer than the best form.
 hipError_t launch_grouped_gemm_fp4(const GemmFp4Launch& L, hipStream_t stream)
 {
     if (L.groups.rows == 0 || L.groups.num == 0)
         return hipSuccess;
-    const int m = L.expected_rows;
-    if (m <= 8)
-        skinny_run<1, 4>(L, stream);
-    else if (m <= 16)
-        skinny_run<2, 4>(L, stream);
-    else if (m <= 64)
-        skinny_run<4, 4>(L, stream);
-    else {
-        debug_launch("grouped_gemm_fp4_tile", dim3(kCus), dim3(512), 0);
-        const bool four = L.K % 512 == 0 && reinterpret_cast<uintptr_t>(L.w_scales) % 16 == 0;
-        auto* kernel = four ? gemm_fp4_tile_kernel<true> : gemm_fp4_tile_kernel<false>;
-        kernel<<<kCus, 512, 0, stream>>>(L);
+    const int64_t m = L.expected_rows, KB = L.K / kQBlock;
+    // tiles on average: a group's last one is half full
+    const auto tiles = [&](int rows, int cols) {
+        const int64_t twice = 2 * m / rows + 1;
+        return L.groups.num * (twice < 2 ? 2 : twice) * ((L.N + cols - 1) / cols) / 2;
+    };
+    const auto rounds = [](int64_t tiles, int64_t room) { return (tiles + room - 1) / room; };
+    const int64_t small = tiles(kSmallRows, kSmallCols) / 7, large = rounds(tiles(kTile, kTile), kCus);
+    const int64_t small_time = 650 + KB * (small > 80 ? small : 80), large_time = 650 + 165 * KB * large;
+    const int64_t B = KB <= kStreamWaves * 4 ? 4 : 8;
+    if (KB <= kStreamWaves * B) {
+        const int64_t r = rounds(tiles(16, kStreamCols), kCus * (kStreamWaves / ((KB + B - 1) / B)));
+        const int64_t time = 800 + r * (225 + 20 * KB);
+        // at one or two rows a group its lead is small, but the model does not see it (82 us against 85 above)
+        if (m <= 2 || ((m <= 16 || r == 1) && time < small_time && time < large_time)) {
+            B == 4 ? stream_run<4>(L, stream) : stream_run<8>(L, stream);
+            return hipGetLastError();
+        }
     }
+    if (small_time <= large_time)
+        small_run(L, stream);
+    else
+        tile_run(L, stream);
     return hipGetLastError();
 }
 

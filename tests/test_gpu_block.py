@@ -518,15 +518,15 @@ COUNTS = {"one": [1], "few": [3, 0, 1, 17, 0], "mixed": [40, 0, 130, 5, 257, 16]
 
 
 @pytest.mark.parametrize("name", sorted(COUNTS))
-@pytest.mark.parametrize("N,K", [(128, 128), (384, 256), (256, 640), (512, 2048)])
-@pytest.mark.parametrize("expected", [2, 12, 100, 100000])
+@pytest.mark.parametrize("N,K", [(128, 128), (384, 256), (256, 640), (512, 2048), (128, 5248)])
+@pytest.mark.parametrize("expected", [1, 12, 40, 100000])
 def test_product_fp4(ep, name, N, K, expected):
     """Every tile form (chosen by the typical rows) on every distribution."""
     _check_product(ep, COUNTS[name], N, K, expected)
 
 
-@pytest.mark.parametrize("expected", [2, 12, 100, 100000])
-@pytest.mark.parametrize("N,K", [(256, 512), (384, 640)])
+@pytest.mark.parametrize("expected", [1, 12, 40, 100000])
+@pytest.mark.parametrize("N,K", [(256, 512), (384, 640), (128, 7168)])
 def test_product_fp4_column_major_scales_and_static_layout(ep, N, K, expected):
     _check_product(ep, [5, 0, 300, 17], N, K, expected, column_major=True)
     _check_product(ep, [5, 0, 33, 17], N, K, expected, stride=33)
@@ -540,7 +540,7 @@ def test_product_fp4_many_groups_and_long_rows(ep):
 
 @pytest.mark.parametrize("off,stride", [([-5, 3, 40, 12, 9], 0), ([0, 1 << 30, -(1 << 30), 20, 2 ** 31 - 1], 0),
                                         ([9, 7, 5, 3, 1], 0), ([0, 1 << 30, 5, 2, 2 ** 31 - 1], 8)])
-@pytest.mark.parametrize("expected", [2, 100000])
+@pytest.mark.parametrize("expected", [2, 40, 100000])
 def test_fp4_offsets_outside_the_rows_are_clamped(ep, off, stride, expected):
     dev = _dev()
     g = _gen(3)
