@@ -98,14 +98,13 @@ def ep_grouped_gemm_fp4(x, x_scales, scale_ld, w, w_scales, group_offsets, num_g
 # the same calls on torch tensors
 # ----------------------------------------------------------------------------
 
-def _rows(t, name):
-    """Elements between the rows of a matrix whose rows are contiguous (they may lie apart)."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a GPU tensor (got device {t.device})")
-    T, H = t.shape
-    if T > 0 and t.stride(1) != 1:
+def _rows(t, T, H, name):
+    """Elements between the rows of a matrix [T, H] whose rows are contiguous (they may lie apart)."""
+    ld, step = t.stride()
+    if T <= 1:
+        ld = H
+    if step != 1 and T > 0 and H > 1:
         raise ValueError(f"the rows of {name} must be contiguous")
-    ld = t.stride(0) if T > 1 else H
     if ld < H or ld % 8:
         raise ValueError(f"{name}: the stride of its rows ({ld}) must be a multiple of 8 and at least {H}")
     return ld
@@ -114,9 +113,9 @@ def _rows(t, name):
 def _f32(t, name):
     """Whether a tensor that may be bf16 or fp32 is fp32."""
     import torch
-    if t.dtype == torch.float32:
+    if t.dtype is torch.float32:
         return 1
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be torch.float32 or torch.bfloat16, got {t.dtype}")
     return 0
 
@@ -125,41 +124,43 @@ def _norm_args(x, y, norm, weight, y_norm, y_weight, gate, residual_scale, y_sca
     import torch
     T, H = _matrix(x, "x")
     _i32(H, "width")
-    a = ep_block_norm_t()
-    a.x_f32 = _f32(x, "x")
+    yp = wp = ywp = gp = None
+    y_ld = weights_f32 = kind = gate_f32 = 0
+    x_f32 = _f32(x, "x")
+    x_ld = _rows(x, T, H, "x")
     if y is not None:
         _shape(y, (T, H), "y")
-        if y.dtype != torch.bfloat16:
+        if y.dtype is not torch.bfloat16:
             raise TypeError(f"y must be torch.bfloat16, got {y.dtype}")
+        yp, y_ld = y.data_ptr(), _rows(y, T, H, "y")
     elif y_norm or y_weight is not None or gate is not None or residual_scale != 1.0 or not norm:
         raise ValueError("without y there is a norm of x alone: y_norm, y_weight, gate and residual_scale need y")
     if weight is not None:
         if not norm:
             raise ValueError("weight needs norm")
         _shape(weight, (H,), "weight")
-        a.weights_f32 = _f32(weight, "weight")
+        weights_f32 = _f32(weight, "weight")
+        wp = _ptr(weight, None, "weight")
     if y_weight is not None:
         _shape(y_weight, (H,), "y_weight")
-        a.weights_f32 = _f32(y_weight, "y_weight")
-        if weight is not None and weight.dtype != y_weight.dtype:
+        weights_f32 = _f32(y_weight, "y_weight")
+        if weight is not None and weight.dtype is not y_weight.dtype:
             raise TypeError(f"weight and y_weight must be of one type, got {weight.dtype} and {y_weight.dtype}")
+        ywp = _ptr(y_weight, None, "y_weight")
     if gate is not None:
-        if gate.shape != (T, 1) and gate.shape != (1, H):
+        kind = EP_GATE_TOKEN if gate.shape == (T, 1) else EP_GATE_CHANNEL
+        if kind == EP_GATE_CHANNEL and gate.shape != (1, H):
             raise ValueError(f"gate must be [{T}, 1] or [1, {H}], got shape {list(gate.shape)}")
-        a.gate_kind = EP_GATE_TOKEN if gate.shape == (T, 1) else EP_GATE_CHANNEL
-        a.gate_f32 = _f32(gate, "gate")
-        a.gate = _ptr(gate, None, "gate")
-    a.x = x.data_ptr()
-    a.x_ld = _rows(x, "x")
-    if y is not None:
-        a.y = y.data_ptr()
-        a.y_ld = _rows(y, "y")
-    a.weight = _ptr(weight, None, "weight")
-    a.y_weight = _ptr(y_weight, None, "y_weight")
-    a.num_rows, a.width = T, H
-    a.norm, a.y_norm = bool(norm), bool(y_norm)
-    a.residual_scale, a.y_scale, a.eps, a.weight_offset = residual_scale, y_scale, eps, weight_offset
-    return a, T, H
+        gate_f32 = _f32(gate, "gate")
+        gp = _ptr(gate, None, "gate")
+    return ep_block_norm_t(x.data_ptr(), yp, wp, ywp, gp, x_ld, y_ld, T, H, x_f32, bool(norm), bool(y_norm),
+                           weights_f32, kind, gate_f32, residual_scale, y_scale, eps, weight_offset), T, H
+
+
+def _empty(t):
+    """A dense tensor of t's shape and type (empty_like costs the host half of what empty does)."""
+    import torch
+    return torch.empty_like(t) if t.is_contiguous() else torch.empty(t.shape, dtype=t.dtype, device=t.device)
 
 
 @dataclass
@@ -199,13 +200,14 @@ def block_norm(x, y=None, *, norm: bool = True, weight=None, y_norm: bool = Fals
             if y is None:
                 raise ValueError("x_out needs y: without it x' is x")
             _shape(x_out, (T, H), "x_out")
-            if x_out.dtype != x.dtype:
+            if x_out.dtype is not x.dtype:
                 raise TypeError(f"x_out must be {x.dtype}, got {x_out.dtype}")
         elif y is not None:
-            x_out = torch.empty((T, H), dtype=x.dtype, device=x.device)
+            x_out = _empty(x)
         h = codes = scales = None
         if norm and write_h:
-            h = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
+            like = y if y is not None else x
+            h = _empty(like) if like.dtype is torch.bfloat16 else torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
         if quantize:
             codes = torch.empty((T, H), dtype=torch.float8_e4m3fn, device=x.device)
             scales = torch.empty((T, H // 128), dtype=torch.float32, device=x.device)
@@ -256,7 +258,7 @@ def block_norm_backward(x, y=None, *, grad_x=None, grad_h=None, norm: bool = Tru
         def new(t, name):
             if t is None or name not in need:
                 return None
-            return torch.empty(t.shape, dtype=t.dtype, device=x.device)
+            return _empty(t)
 
         o = BlockNormGrads(new(x, "x"), new(y, "y"), new(weight, "weight"), new(y_weight, "y_weight"),
                            new(gate, "gate"))

@@ -11,8 +11,8 @@
 namespace moe_ep {
 
 constexpr int kTeamWaves = 16;               // waves of a row, at most
-constexpr int kForwardBlocks = 2048;
-constexpr int kBackwardBlocks = 512;
+constexpr int kForwardBlocks = 1024;
+constexpr int kBackwardBlocks = 256;
 
 template <int CTRL>
 __device__ __forceinline__ float dpp_f(float v)
@@ -68,26 +68,24 @@ struct TeamSum {
     }
 };
 
-// Eight channels of a vector of parameters.
-__device__ __forceinline__ void load_param8(const void* p, bool f32, int vec, float (&v)[8])
-{
-    if (f32) {
-        const u32x4 a = load16_hint<false>(static_cast<const float*>(p) + 8 * vec);
-        const u32x4 b = load16_hint<false>(static_cast<const float*>(p) + 8 * vec + 4);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            v[j] = __uint_as_float(a[j]);
-            v[4 + j] = __uint_as_float(b[j]);
-        }
-    } else {
-        const u32x4 a = load16_hint<false>(static_cast<const uint16_t*>(p) + 8 * vec);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            v[2 * j] = bf16_lo(a[j]);
-            v[2 * j + 1] = bf16_hi(a[j]);
-        }
+// Eight channels of a vector of parameters as they lie in memory (fp32, or bf16 twice).
+// Loading and widening are apart, so that all loads are on their way before one is waited for.
+struct RawParam8 {
+    u32x4 d[2] = {u32x4{0u, 0u, 0u, 0u}, u32x4{0u, 0u, 0u, 0u}};
+
+    __device__ __forceinline__ void load(const void* p, bool f32, int vec)
+    {
+        const char* q = static_cast<const char*>(p) + (size_t)vec * (f32 ? 32 : 16);
+        d[0] = load16_hint<false>(q);
+        d[1] = load16_hint<false>(q + (f32 ? 16 : 0));
     }
-}
+    __device__ __forceinline__ float get(bool f32, int j) const
+    {
+        const float wide = __uint_as_float(d[j >> 2][j & 3]);
+        const float narrow = (j & 1) ? bf16_hi(d[0][j >> 1]) : bf16_lo(d[0][j >> 1]);
+        return f32 ? wide : narrow;
+    }
+};
 
 __device__ __forceinline__ float load_param(const void* p, bool f32, int i)
 {
@@ -104,39 +102,30 @@ __device__ __forceinline__ void store_param(void* p, bool f32, int i, float v)
         static_cast<uint16_t*>(p)[i] = (uint16_t)f32_to_bf16_rne(v);
 }
 
-// Factors of y and of the norm in eight channels.
-__device__ __forceinline__ void y_factors(const ep_block_norm_t& a, int vec, float (&f)[8])
-{
-    float t[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-        f[j] = a.y_scale;
-    if (a.y_weight) {
-        load_param8(a.y_weight, a.weights_f32, vec, t);
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            f[j] *= a.weight_offset + t[j];
-    }
-    if (a.gate_kind == EP_GATE_CHANNEL) {
-        load_param8(a.gate, a.gate_f32, vec, t);
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            f[j] *= t[j];
-    }
-}
+// The parameters of eight channels, and what they make up: y's factor and the norm's.
+struct Factors8 {
+    RawParam8 yw, gate, w;
 
-__device__ __forceinline__ void norm_factors(const ep_block_norm_t& a, int vec, float (&f)[8])
-{
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-        f[j] = 1.0f;
-    if (a.weight) {
-        load_param8(a.weight, a.weights_f32, vec, f);
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            f[j] += a.weight_offset;
+    __device__ __forceinline__ void load(const ep_block_norm_t& a, int vec)
+    {
+        if (a.y_weight)
+            yw.load(a.y_weight, a.weights_f32, vec);
+        if (a.gate_kind == EP_GATE_CHANNEL)
+            gate.load(a.gate, a.gate_f32, vec);
+        if (a.weight)
+            w.load(a.weight, a.weights_f32, vec);
     }
-}
+    __device__ __forceinline__ void get(const ep_block_norm_t& a, float (&fy)[8], float (&fw)[8]) const
+    {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            fy[j] = a.y_weight ? a.y_scale * (a.weight_offset + yw.get(a.weights_f32, j)) : a.y_scale;
+            if (a.gate_kind == EP_GATE_CHANNEL)
+                fy[j] *= gate.get(a.gate_f32, j);
+            fw[j] = a.weight ? a.weight_offset + w.get(a.weights_f32, j) : 1.0f;
+        }
+    }
+};
 
 // Eight values of a row as they lie in memory: bf16 or fp32.
 template <bool F32>
@@ -191,34 +180,45 @@ __global__ __launch_bounds__(THREADS) void block_norm_kernel(BlockNormLaunch L)
     const int first = WAVE ? blockIdx.x * (THREADS / kWave) + threadIdx.x / kWave : blockIdx.x;
     const float inv = 1.0f / (float)H;
     TeamSum<WAVE, 1> sum{slots, 0};
-    float fy[V][8], fw[V][8];
     bool on[V];
+    Factors8 f[V];
+    Raw8<F32> nx[V];
+    Raw8<false> ny[V];
+    // a row on its way while the one before it is computed
+    const auto fetch = [&](int64_t row) {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (on[i]) {
+                const int c = (lane + i * lanes) * 8;
+                nx[i].load(a.x, row * a.x_ld + c);
+                if (a.y)
+                    ny[i].load(a.y, row * a.y_ld + c);
+            }
+    };
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         on[i] = lane + i * lanes < vecs;
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            fy[i][j] = fw[i][j] = 0.0f;
-        if (on[i]) {
-            if (a.y)
-                y_factors(a, lane + i * lanes, fy[i]);
-            norm_factors(a, lane + i * lanes, fw[i]);
-        }
+        nx[i].zero();
+        ny[i].zero();
+        if (on[i])
+            f[i].load(a, lane + i * lanes);
     }
+    if (first < a.num_rows)
+        fetch(first);
+    float fy[V][8], fw[V][8];
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        f[i].get(a, fy[i], fw[i]);
     for (int64_t row = first; row < a.num_rows; row += teams) {
         Raw8<F32> x[V];
         Raw8<false> y[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            x[i].zero();
-            y[i].zero();
-            if (on[i]) {
-                const int c = (lane + i * lanes) * 8;
-                x[i].load(a.x, row * a.x_ld + c);
-                if (a.y)
-                    y[i].load(a.y, row * a.y_ld + c);
-            }
+            x[i] = nx[i];
+            y[i] = ny[i];
         }
+        if (row + teams < a.num_rows)
+            fetch(row + teams);
         float v[V][8];
         float ss[1] = {0.0f};
         if (a.y) {
@@ -312,41 +312,56 @@ __global__ __launch_bounds__(THREADS) void block_norm_backward_kernel(BlockNormB
     const int first = WAVE ? blockIdx.x * (THREADS / kWave) + threadIdx.x / kWave : blockIdx.x;
     const float inv = 1.0f / (float)H;
     TeamSum<WAVE, 2> sum{slots, 0};
-    float fy[V][8], fw[V][8], P[V][8], S[V][8];
     bool on[V];
+    Factors8 f[V];
+    Raw8<F32> nx[V], ngx[V];
+    Raw8<false> ny[V], ngh[V];
+    const auto fetch = [&](int64_t row) {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (on[i]) {
+                const int c = (lane + i * lanes) * 8;
+                nx[i].load(a.x, row * a.x_ld + c);
+                if (a.y)
+                    ny[i].load(a.y, row * a.y_ld + c);
+                if (L.gx)
+                    ngx[i].load(L.gx, row * H + c);
+                if (L.gh)
+                    ngh[i].load(L.gh, row * H + c);
+            }
+    };
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         on[i] = lane + i * lanes < vecs;
+        nx[i].zero();
+        ny[i].zero();
+        ngx[i].zero();
+        ngh[i].zero();
+        if (on[i])
+            f[i].load(a, lane + i * lanes);
+    }
+    if (first < a.num_rows)
+        fetch(first);
+    float fy[V][8], fw[V][8], P[V][8], S[V][8];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        f[i].get(a, fy[i], fw[i]);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            fy[i][j] = fw[i][j] = P[i][j] = S[i][j] = 0.0f;
-        if (on[i]) {
-            if (a.y)
-                y_factors(a, lane + i * lanes, fy[i]);
-            if (a.norm)
-                norm_factors(a, lane + i * lanes, fw[i]);
-        }
+            P[i][j] = S[i][j] = 0.0f;
     }
     for (int64_t row = first; row < a.num_rows; row += teams) {
         Raw8<F32> x[V], gx[V];
         Raw8<false> y[V], gh[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            x[i].zero();
-            y[i].zero();
-            gx[i].zero();
-            gh[i].zero();
-            if (on[i]) {
-                const int c = (lane + i * lanes) * 8;
-                x[i].load(a.x, row * a.x_ld + c);
-                if (a.y)
-                    y[i].load(a.y, row * a.y_ld + c);
-                if (L.gx)
-                    gx[i].load(L.gx, row * H + c);
-                if (L.gh)
-                    gh[i].load(L.gh, row * H + c);
-            }
+            x[i] = nx[i];
+            y[i] = ny[i];
+            gx[i] = ngx[i];
+            gh[i] = ngh[i];
         }
+        if (row + teams < a.num_rows)
+            fetch(row + teams);
         float rz = 1.0f, gt = 1.0f;
         if (a.y_norm) {
             float ss[2] = {0.0f, 0.0f};
@@ -460,25 +475,43 @@ __global__ __launch_bounds__(THREADS) void block_norm_backward_kernel(BlockNormB
     }
 }
 
-// The workgroups' sums, added in their order: 64 columns a workgroup, four of its
-// waves share the list.
-__global__ __launch_bounds__(256) void block_norm_reduce_kernel(BlockNormBackwardLaunch L, int blocks)
+// The workgroups' sums: 64 columns a workgroup.  Sixteen lanes read a list entry's 64
+// columns, so the workgroup takes 64 entries at a time; entry b goes to share b % 64, and
+// the shares are added in their order.
+constexpr int kReduceThreads = 1024, kShares = kReduceThreads / 16;
+
+__global__ __launch_bounds__(kReduceThreads) void block_norm_reduce_kernel(BlockNormBackwardLaunch L, int blocks)
 {
-    __shared__ float got[4][kWave];
+    __shared__ float got[kShares][kWave + 4];
     const ep_block_norm_t& a = L.in;
-    const int H = a.width, lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
-    const int which = blockIdx.y, c = blockIdx.x * kWave + lane;
+    const int H = a.width, which = blockIdx.y, c0 = blockIdx.x * kWave;
     if (which == 0 ? !L.dw : !(L.dyw || (L.dgate && a.gate_kind == EP_GATE_CHANNEL)))
         return;
-    float v = 0.0f;
-    if (c < H)
-        for (int b = wave; b < blocks; b += 4)
-            v += L.part[((size_t)b * 2 + which) * H + c];
+    const int share = threadIdx.x / 16, at = (threadIdx.x % 16) * 4;
+    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (c0 + at < H)                       // widths are multiples of eight: all four columns exist
+        for (int b = share; b < blocks; b += kShares) {
+            const u32x4 d = load16_hint<false>(L.part + ((size_t)b * 2 + which) * H + c0 + at);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                s[j] += __uint_as_float(d[j]);
+        }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        got[share][at + j] = s[j];
+    __syncthreads();
+    // wave w adds shares 4 w .. 4 w + 3, the first wave the sixteen sums
+    const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave, c = c0 + lane;
+    float v = (got[4 * wave][lane] + got[4 * wave + 1][lane]) + (got[4 * wave + 2][lane] + got[4 * wave + 3][lane]);
+    __syncthreads();
     got[wave][lane] = v;
     __syncthreads();
     if (wave || c >= H)
         return;
-    v = (got[0][lane] + got[1][lane]) + (got[2][lane] + got[3][lane]);
+    v = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kReduceThreads / kWave; ++w)
+        v += got[w][lane];
     if (which == 0) {
         store_param(L.dw, a.weights_f32, c, v);
         return;
@@ -569,8 +602,8 @@ hipError_t launch_block_norm_backward(const BlockNormBackwardLaunch& L, hipStrea
     }
     if (L.part) {
         const dim3 grid((L.in.width + kWave - 1) / kWave, 2);
-        debug_launch("block_norm_reduce", grid, dim3(256), 0);
-        block_norm_reduce_kernel<<<grid, 256, 0, stream>>>(L, blocks);
+        debug_launch("block_norm_reduce", grid, dim3(kReduceThreads), 0);
+        block_norm_reduce_kernel<<<grid, kReduceThreads, 0, stream>>>(L, blocks);
     }
     return hipGetLastError();
 }
