@@ -11,8 +11,8 @@
 namespace moe_ep {
 
 constexpr int kTeamWaves = 16;               // waves of a row, at most
-constexpr int kForwardBlocks = 1024;
-constexpr int kBackwardBlocks = 256;
+constexpr int kCus = 256;
+constexpr int64_t kLargeBytes = (int64_t)160 << 20;
 
 template <int CTRL>
 __device__ __forceinline__ float dpp_f(float v)
@@ -106,23 +106,73 @@ __device__ __forceinline__ void store_param(void* p, bool f32, int i, float v)
 struct Factors8 {
     RawParam8 yw, gate, w;
 
-    __device__ __forceinline__ void load(const ep_block_norm_t& a, int vec)
+    __device__ __forceinline__ void load_y(const ep_block_norm_t& a, int vec)
     {
         if (a.y_weight)
             yw.load(a.y_weight, a.weights_f32, vec);
         if (a.gate_kind == EP_GATE_CHANNEL)
             gate.load(a.gate, a.gate_f32, vec);
+    }
+    __device__ __forceinline__ void load_w(const ep_block_norm_t& a, int vec)
+    {
         if (a.weight)
             w.load(a.weight, a.weights_f32, vec);
     }
-    __device__ __forceinline__ void get(const ep_block_norm_t& a, float (&fy)[8], float (&fw)[8]) const
+    __device__ __forceinline__ void get_y(const ep_block_norm_t& a, float (&fy)[8]) const
     {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             fy[j] = a.y_weight ? a.y_scale * (a.weight_offset + yw.get(a.weights_f32, j)) : a.y_scale;
             if (a.gate_kind == EP_GATE_CHANNEL)
                 fy[j] *= gate.get(a.gate_f32, j);
+        }
+    }
+    __device__ __forceinline__ void get_w(const ep_block_norm_t& a, float (&fw)[8]) const
+    {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
             fw[j] = a.weight ? a.weight_offset + w.get(a.weights_f32, j) : 1.0f;
+    }
+};
+
+// A lane's factors: kept in registers, or, in rows wider than 8192 (1024 threads, 128
+// registers each), read again from memory at each use.
+template <int V, bool KEEP>
+struct Factors {
+    float y[KEEP ? V : 1][8], w[KEEP ? V : 1][8];
+
+    __device__ __forceinline__ void keep(const ep_block_norm_t& a, const Factors8 (&f)[V])
+    {
+#pragma unroll
+        for (int i = 0; i < (KEEP ? V : 0); ++i) {
+            f[i].get_y(a, y[i]);
+            f[i].get_w(a, w[i]);
+        }
+    }
+    __device__ __forceinline__ void get_y(const ep_block_norm_t& a, int i, int vec, bool on, float (&o)[8]) const
+    {
+        if (KEEP) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                o[j] = y[KEEP ? i : 0][j];
+        } else {
+            Factors8 f;
+            if (on)
+                f.load_y(a, vec);
+            f.get_y(a, o);
+        }
+    }
+    __device__ __forceinline__ void get_w(const ep_block_norm_t& a, int i, int vec, bool on, float (&o)[8]) const
+    {
+        if (KEEP) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                o[j] = w[KEEP ? i : 0][j];
+        } else {
+            Factors8 f;
+            if (on)
+                f.load_w(a, vec);
+            f.get_w(a, o);
         }
     }
 };
@@ -151,25 +201,26 @@ struct Raw8 {
             return __uint_as_float(d[F32 ? j >> 2 : 0][j & 3]);
         return (j & 1) ? bf16_hi(d[0][j >> 1]) : bf16_lo(d[0][j >> 1]);
     }
+    template <bool NT = false>
     static __device__ __forceinline__ void store(void* p, size_t at, const float (&v)[8])
     {
         char* q = static_cast<char*>(p) + at * (F32 ? 4 : 2);
         if (F32) {
 #pragma unroll
             for (int i = 0; i < 2; ++i)
-                store16_hint<false>(q + 16 * i, u32x4{__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]),
+                store16_hint<NT>(q + 16 * i, u32x4{__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]),
                                                       __float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3])});
         } else {
             u32x4 o;
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 o[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
-            store16_hint<false>(q, o);
+            store16_hint<NT>(q, o);
         }
     }
 };
 
-template <bool WAVE, int V, bool F32, int THREADS>
+template <bool WAVE, int V, bool F32, int THREADS, bool NT>
 __global__ __launch_bounds__(THREADS) void block_norm_kernel(BlockNormLaunch L)
 {
     __shared__ float slots[2][kTeamWaves][1];
@@ -180,8 +231,10 @@ __global__ __launch_bounds__(THREADS) void block_norm_kernel(BlockNormLaunch L)
     const int first = WAVE ? blockIdx.x * (THREADS / kWave) + threadIdx.x / kWave : blockIdx.x;
     const float inv = 1.0f / (float)H;
     TeamSum<WAVE, 1> sum{slots, 0};
+    constexpr bool KEEP = THREADS <= 512;
     bool on[V];
-    Factors8 f[V];
+    Factors8 f[KEEP ? V : 1];
+    Factors<V, KEEP> factors;
     Raw8<F32> nx[V];
     Raw8<false> ny[V];
     // a row on its way while the one before it is computed
@@ -200,16 +253,18 @@ __global__ __launch_bounds__(THREADS) void block_norm_kernel(BlockNormLaunch L)
         on[i] = lane + i * lanes < vecs;
         nx[i].zero();
         ny[i].zero();
-        if (on[i])
-            f[i].load(a, lane + i * lanes);
+        if (KEEP && on[i]) {
+            f[KEEP ? i : 0].load_y(a, lane + i * lanes);
+            f[KEEP ? i : 0].load_w(a, lane + i * lanes);
+        }
     }
-    if (first < a.num_rows)
+    if (KEEP && first < a.num_rows)
         fetch(first);
-    float fy[V][8], fw[V][8];
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-        f[i].get(a, fy[i], fw[i]);
+    if constexpr (KEEP)
+        factors.keep(a, f);
     for (int64_t row = first; row < a.num_rows; row += teams) {
+        if (!KEEP)
+            fetch(row);
         Raw8<F32> x[V];
         Raw8<false> y[V];
 #pragma unroll
@@ -217,7 +272,7 @@ __global__ __launch_bounds__(THREADS) void block_norm_kernel(BlockNormLaunch L)
             x[i] = nx[i];
             y[i] = ny[i];
         }
-        if (row + teams < a.num_rows)
+        if (KEEP && row + teams < a.num_rows)
             fetch(row + teams);
         float v[V][8];
         float ss[1] = {0.0f};
@@ -236,11 +291,13 @@ __global__ __launch_bounds__(THREADS) void block_norm_kernel(BlockNormLaunch L)
                 cy *= load_param(a.gate, a.gate_f32, (int)row);
 #pragma unroll
             for (int i = 0; i < V; ++i) {
+                float fy[8];
+                factors.get_y(a, i, lane + i * lanes, on[i], fy);
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                    v[i][j] = __builtin_fmaf(a.residual_scale, x[i].get(j), y[i].get(j) * cy * fy[i][j]);
+                    v[i][j] = __builtin_fmaf(a.residual_scale, x[i].get(j), y[i].get(j) * cy * fy[j]);
                 if (L.xo && on[i])
-                    Raw8<F32>::store(L.xo, row * H + (lane + i * lanes) * 8, v[i]);
+                    Raw8<F32>::template store<NT>(L.xo, row * H + (lane + i * lanes) * 8, v[i]);
             }
         } else {
 #pragma unroll
@@ -262,11 +319,13 @@ __global__ __launch_bounds__(THREADS) void block_norm_kernel(BlockNormLaunch L)
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int vec = lane + i * lanes;
+            float fw[8];
+            factors.get_w(a, i, vec, on[i], fw);
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                v[i][j] = v[i][j] * r * fw[i][j];
+                v[i][j] = v[i][j] * r * fw[j];
             if (L.h && on[i])
-                Raw8<false>::store(L.h, row * H + vec * 8, v[i]);
+                Raw8<false>::template store<NT>(L.h, row * H + vec * 8, v[i]);
             if (L.codes) {
                 // sixteen lanes hold a block of 128 (all of them on, or none)
                 float m = 0.0f;
@@ -312,8 +371,10 @@ __global__ __launch_bounds__(THREADS) void block_norm_backward_kernel(BlockNormB
     const int first = WAVE ? blockIdx.x * (THREADS / kWave) + threadIdx.x / kWave : blockIdx.x;
     const float inv = 1.0f / (float)H;
     TeamSum<WAVE, 2> sum{slots, 0};
+    constexpr bool KEEP = THREADS <= 512;
     bool on[V];
-    Factors8 f[V];
+    Factors8 f[KEEP ? V : 1];
+    Factors<V, KEEP> factors;
     Raw8<F32> nx[V], ngx[V];
     Raw8<false> ny[V], ngh[V];
     const auto fetch = [&](int64_t row) {
@@ -337,20 +398,24 @@ __global__ __launch_bounds__(THREADS) void block_norm_backward_kernel(BlockNormB
         ny[i].zero();
         ngx[i].zero();
         ngh[i].zero();
-        if (on[i])
-            f[i].load(a, lane + i * lanes);
+        if (KEEP && on[i]) {
+            f[KEEP ? i : 0].load_y(a, lane + i * lanes);
+            f[KEEP ? i : 0].load_w(a, lane + i * lanes);
+        }
     }
-    if (first < a.num_rows)
+    if (KEEP && first < a.num_rows)
         fetch(first);
-    float fy[V][8], fw[V][8], P[V][8], S[V][8];
+    if constexpr (KEEP)
+        factors.keep(a, f);
+    float P[V][8], S[V][8];
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        f[i].get(a, fy[i], fw[i]);
+    for (int i = 0; i < V; ++i)
 #pragma unroll
         for (int j = 0; j < 8; ++j)
             P[i][j] = S[i][j] = 0.0f;
-    }
     for (int64_t row = first; row < a.num_rows; row += teams) {
+        if (!KEEP)
+            fetch(row);
         Raw8<F32> x[V], gx[V];
         Raw8<false> y[V], gh[V];
 #pragma unroll
@@ -360,7 +425,7 @@ __global__ __launch_bounds__(THREADS) void block_norm_backward_kernel(BlockNormB
             gx[i] = ngx[i];
             gh[i] = ngh[i];
         }
-        if (row + teams < a.num_rows)
+        if (KEEP && row + teams < a.num_rows)
             fetch(row + teams);
         float rz = 1.0f, gt = 1.0f;
         if (a.y_norm) {
@@ -386,25 +451,32 @@ __global__ __launch_bounds__(THREADS) void block_norm_backward_kernel(BlockNormB
             float ss[2] = {0.0f, 0.0f};
             const float cy = rz * gt;
 #pragma unroll
-            for (int i = 0; i < V; ++i)
+            for (int i = 0; i < V; ++i) {
+                float fy[8], fw[8];
+                factors.get_y(a, i, lane + i * lanes, on[i], fy);
+                factors.get_w(a, i, lane + i * lanes, on[i], fw);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    v[i][j] = a.y ? __builtin_fmaf(a.residual_scale, x[i].get(j), y[i].get(j) * cy * fy[i][j])
+                    v[i][j] = a.y ? __builtin_fmaf(a.residual_scale, x[i].get(j), y[i].get(j) * cy * fy[j])
                                   : x[i].get(j);
                     ss[0] = __builtin_fmaf(v[i][j], v[i][j], ss[0]);
-                    ss[1] = __builtin_fmaf(gh[i].get(j) * fw[i][j], v[i][j], ss[1]);
+                    ss[1] = __builtin_fmaf(gh[i].get(j) * fw[j], v[i][j], ss[1]);
                 }
+            }
             sum(ss);
             const float r = __builtin_amdgcn_rsqf(ss[0] * inv + a.eps);
             const float k = r * ss[1] * inv;
 #pragma unroll
-            for (int i = 0; i < V; ++i)
+            for (int i = 0; i < V; ++i) {
+                float fw[8];
+                factors.get_w(a, i, lane + i * lanes, on[i], fw);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     const float xh = v[i][j] * r;
                     P[i][j] = __builtin_fmaf(gh[i].get(j), xh, P[i][j]);
-                    g[i][j] = __builtin_fmaf(r, gh[i].get(j) * fw[i][j] - xh * k, g[i][j]);
+                    g[i][j] = __builtin_fmaf(r, gh[i].get(j) * fw[j] - xh * k, g[i][j]);
                 }
+            }
         }
         if (L.dx) {
 #pragma unroll
@@ -421,14 +493,17 @@ __global__ __launch_bounds__(THREADS) void block_norm_backward_kernel(BlockNormB
             continue;
         float ss[2] = {0.0f, 0.0f};
 #pragma unroll
-        for (int i = 0; i < V; ++i)
+        for (int i = 0; i < V; ++i) {
+            float fy[8];
+            factors.get_y(a, i, lane + i * lanes, on[i], fy);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const float z = y[i].get(j) * rz;
                 S[i][j] = __builtin_fmaf(gt * g[i][j], z, S[i][j]);
-                g[i][j] *= fy[i][j];
+                g[i][j] *= fy[j];
                 ss[0] = __builtin_fmaf(g[i][j], z, ss[0]);
             }
+        }
         if (a.y_norm || (L.dgate && a.gate_kind == EP_GATE_TOKEN))
             sum(ss);
         if (L.dgate && a.gate_kind == EP_GATE_TOKEN && lane == 0)
@@ -526,7 +601,8 @@ __global__ __launch_bounds__(kReduceThreads) void block_norm_reduce_kernel(Block
 }
 
 // The team of a row and the workgroups: a wave with one or two vectors of eight a lane
-// up to a width of 1024, else a workgroup with one vector up to 2048, two up to 16384.
+// up to a width of 1024, else a workgroup with one vector up to 2048, two up to
+// 16384, then four.
 struct Team {
     bool wave;
     int v, threads;
@@ -535,6 +611,8 @@ struct Team {
         const int64_t need = wave ? ((int64_t)rows + 3) / 4 : rows;
         return (int)(need < most ? need : most);
     }
+    // backward: as many workgroups as a CU holds at once (eight waves of 200 registers)
+    int backward_blocks(int rows) const { return blocks(rows, kCus * (threads <= 256 ? 2 : 1)); }
 };
 
 static Team team_of(int width)
@@ -569,7 +647,11 @@ static hipError_t run_team(const char* name, const Team& t, const L& args, int b
 
 template <bool WAVE, int V, bool F32, int THREADS>
 struct Forward {
-    static auto get() { return block_norm_kernel<WAVE, V, F32, THREADS>; }
+    static auto get() { return block_norm_kernel<WAVE, V, F32, THREADS, false>; }
+};
+template <bool WAVE, int V, bool F32, int THREADS>
+struct ForwardLarge {
+    static auto get() { return block_norm_kernel<WAVE, V, F32, THREADS, true>; }
 };
 template <bool WAVE, int V, bool F32, int THREADS>
 struct Backward {
@@ -581,19 +663,24 @@ hipError_t launch_block_norm(const BlockNormLaunch& L, hipStream_t stream)
     if (L.in.num_rows == 0)
         return hipSuccess;
     const Team t = team_of(L.in.width);
-    return run_team<BlockNormLaunch, Forward>("block_norm", t, L, t.blocks(L.in.num_rows, kForwardBlocks), 0, stream);
+    const int blocks = t.blocks(L.in.num_rows, kCus * (t.v == 1 || t.wave ? 4 : 2));
+    // outputs that do not stay in the Infinity Cache anyway pass it by
+    const int64_t bytes = (int64_t)L.in.num_rows * L.in.width * ((L.xo ? L.in.x_f32 ? 4 : 2 : 0) + (L.h ? 2 : 0));
+    if (bytes > kLargeBytes)
+        return run_team<BlockNormLaunch, ForwardLarge>("block_norm", t, L, blocks, 0, stream);
+    return run_team<BlockNormLaunch, Forward>("block_norm", t, L, blocks, 0, stream);
 }
 
 size_t block_norm_workspace(int rows, int width)
 {
-    const int blocks = team_of(width).blocks(rows, kBackwardBlocks);
+    const int blocks = team_of(width).backward_blocks(rows);
     return ((size_t)(blocks ? blocks : 1) * 2 * width * sizeof(float) + 255) / 256 * 256;
 }
 
 hipError_t launch_block_norm_backward(const BlockNormBackwardLaunch& L, hipStream_t stream)
 {
     const Team t = team_of(L.in.width);
-    const int blocks = t.blocks(L.in.num_rows, kBackwardBlocks);
+    const int blocks = t.backward_blocks(L.in.num_rows);
     if (blocks) {
         const size_t lds = t.wave && L.part ? (size_t)2 * L.in.width * sizeof(float) : 0;
         const hipError_t e = run_team<BlockNormBackwardLaunch, Backward>("block_norm_backward", t, L, blocks, lds, stream);
