@@ -18,6 +18,11 @@ requires grad).  Receive rows that no pair maps to get a zero gradient.
     out = experts(x, g.topk_idx, g.topk_weights, w1, w2, P)
     (task_loss(out) + g.loss).backward()
 
+and ``block_norm`` for what lies between two layers, with gradients of the residual
+stream, the block's output, the norms' weights and the gate:
+
+    n = block_norm(x, out, weight=w)                           # n.x: the new stream, n.h: its norm
+
 ``experts`` is dispatch, the two FP8 products with SwiGLU between them, and
 combine.  It keeps what the wanted gradients read: activations in 8 bits (the
 dispatched rows, SwiGLU's input and output), and, only where topk_weights needs
@@ -30,7 +35,7 @@ calls.
 Only argument marshalling happens here; every step runs in the HIP kernels.
 These functions are for eager autograd: a backward pass captured into a graph
 while an eager graph of the same leaves is alive ends the process in torch, so
-``gate`` and ``experts`` refuse to be captured, forward and backward (the plain
+``gate``, ``experts`` and ``block_norm`` refuse to be captured, forward and backward (the plain
 calls they are made of can be).  None of them has a second derivative: asking for one raises.
 """
 from __future__ import annotations
@@ -47,7 +52,9 @@ from . import dispatch_backward as _dispatch_backward
 from . import gate as _gate_call
 from . import gate_backward as _gate_backward
 from . import get_dispatch_layout as _get_dispatch_layout
-from . import (Gate, grouped_gemm_fp8, grouped_wgrad_fp8, quantize_rows, quantize_weights, swiglu_fp8,
+from . import block_norm as _block_norm_call
+from . import block_norm_backward as _block_norm_backward
+from . import (BlockNorm, Gate, grouped_gemm_fp8, grouped_wgrad_fp8, quantize_rows, quantize_weights, swiglu_fp8,
                swiglu_fp8_backward)
 from .experts import _on
 
@@ -263,3 +270,45 @@ def experts(x, topk_idx, topk_weights, w1, w2, num_partitions: int = 1):
         layout = _get_dispatch_layout(topk_idx, E, num_partitions)
         # inside forward gradients are always off
         return _Experts.apply(x, topk_weights, w1, w2, layout, torch.is_grad_enabled())
+
+
+class _BlockNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, y, weight, y_weight, gate, options):
+        # the inputs alone are kept: backward computes both norms' factors again
+        inputs = x, y, weight, y_weight, gate
+        ctx.save_for_backward(*inputs)
+        ctx.options = options
+        ctx.set_materialize_grads(False)
+        x, y, weight, y_weight, gate = (None if t is None else t.detach() for t in inputs)
+        n = _block_norm_call(x, y, weight=weight, y_weight=y_weight, gate=gate, **options)
+        return (None if y is None else n.x), n.h
+
+    @staticmethod
+    @_first_order
+    def backward(ctx, grad_x, grad_h):
+        _eager_only("the backward pass of block_norm")
+        need = [n for n, wanted in zip(_NORM_INPUTS, ctx.needs_input_grad) if wanted]
+        inputs = {n: None if t is None else t.detach() for n, t in zip(_NORM_INPUTS, ctx.saved_tensors)}
+        g = _block_norm_backward(grad_x=None if grad_x is None else grad_x.contiguous(),
+                                 grad_h=None if grad_h is None else grad_h.contiguous(),
+                                 need=need, **inputs, **ctx.options)
+        return (*(getattr(g, n) for n in _NORM_INPUTS), None)
+
+
+_NORM_INPUTS = ("x", "y", "weight", "y_weight", "gate")
+
+
+def block_norm(x, y=None, *, norm: bool = True, weight=None, y_norm: bool = False, y_weight=None, gate=None,
+               residual_scale: float = 1.0, y_scale: float = 1.0, eps: float = 1e-6, weight_offset: float = 0.0):
+    """The norms before and after a block (the plain call's arguments, without its 8-bit
+    rows: ``experts`` makes its own) with gradients for x, y, weight, y_weight and gate.
+    Returns ``BlockNorm``: the new residual stream (x itself without y) and its norm (None
+    without norm).  The inputs are kept for backward: changing one of them in place
+    before is an error."""
+    options = dict(norm=norm, y_norm=y_norm, residual_scale=residual_scale, y_scale=y_scale, eps=eps,
+                   weight_offset=weight_offset)
+    with _on(x, y, weight, y_weight, gate):
+        _eager_only("block_norm")
+        x_out, h = _BlockNorm.apply(x, y, weight, y_weight, gate, options)
+    return BlockNorm(x if y is None else x_out, h)

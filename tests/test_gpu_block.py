@@ -133,9 +133,9 @@ def _check_norm_backward(ep, o, seed=0, norm=True, with_gx=True, with_gh=True):
     G, M = (gx.double(), gx.double().abs()) if gx is not None else (zero, zero)
     E = zero                                               # error of g
     r, kap = f["r"], f["kap"]
-    # a sum over tokens: the rows of a workgroup (each of 512 takes its share; a wave's rows and four waves when narrow),
-    # then the workgroups in four chains
-    depth = T / 512 + 8 + 128 + 3
+    # a sum over tokens: the rows of a workgroup (256 of them or more share the rows; four waves meet when narrow), up to
+    # eight workgroups of a share, four shares of a wave, sixteen waves
+    depth = T / 256 + 1 + 4 + 8 + 4 + 16
     if gh is not None:
         ghd = gh.double()
         d, xh, Xh = ghd * f["w"], f["v"] * r, f["X"] * r
