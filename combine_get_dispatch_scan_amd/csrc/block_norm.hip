@@ -5,6 +5,12 @@
 // and their gradients.  A team of lanes (a wave, or a workgroup of up to 16) holds a
 // row in registers, so every value is read and written once; means are fp32 sums
 // over the lanes.  All arithmetic is fp32, and every output is rounded once.
+//
+// Memory bounds both: 16384 x 7168 in bf16 with y's norm, weights, a token gate and 8-bit
+// rows takes 190 us forward, 5.6 TB/s (a copy of 1 GiB: 5.1), and 298 us backward, 4.7 TB/s.
+// To keep it busy a team fetches its next row before it computes the one it has, and
+// parameters are widened after all of them are on their way (with the wide loads of the
+// second launch: 298 us, 373 before).  One row takes 4.6 us, of which the launch is most.
 #include "block_launch.h"
 #include "quant16.h"
 
@@ -12,7 +18,7 @@ namespace moe_ep {
 
 constexpr int kTeamWaves = 16;               // waves of a row, at most
 constexpr int kCus = 256;
-constexpr int64_t kLargeBytes = (int64_t)160 << 20;
+constexpr int64_t kSmallBytes = (int64_t)16 << 20, kLargeBytes = (int64_t)256 << 20;
 
 template <int CTRL>
 __device__ __forceinline__ float dpp_f(float v)
@@ -135,8 +141,8 @@ struct Factors8 {
     }
 };
 
-// A lane's factors: kept in registers, or, in rows wider than 8192 (1024 threads, 128
-// registers each), read again from memory at each use.
+// A lane's factors: kept in registers, or, in rows wider than 8192 (up to 1024 threads,
+// 128 registers each), read again from memory at each use.
 template <int V, bool KEEP>
 struct Factors {
     float y[KEEP ? V : 1][8], w[KEEP ? V : 1][8];
@@ -357,13 +363,18 @@ __global__ __launch_bounds__(THREADS) void block_norm_kernel(BlockNormLaunch L)
 //   dy = rz gt (g fy - z s / width)   (without y's norm: gt g fy)
 //   dweight = sum over rows of gh x' r;  S = sum over rows of gt g z, from which
 //   dy_weight = b * channel gate * S and the channel gate's gradient b (o + y_weight) S
-// The sums over rows stay in the registers of the workgroups, which take rows in a
-// fixed order, and are added by a second launch.
+// The sums over rows stay in the registers of the workgroups (in LDS in rows of 8200 to
+// 16384: 4096 x 16384 323 us, 356 with registers, which spill), which take rows in a
+// fixed order, and are added by a second launch.  Stores go through the caches, unlike
+// forward ones: with readers of dx and dy behind them that is as fast or faster at every
+// size (8192 x 4096: 121 us, 134 around them).
 template <bool WAVE, int V, bool F32, int THREADS>
 __global__ __launch_bounds__(THREADS) void block_norm_backward_kernel(BlockNormBackwardLaunch L)
 {
     __shared__ float slots[2][kTeamWaves][2];
-    extern __shared__ float comb[];             // WAVE: [2][width], where the waves' sums meet
+    // [2][width].  WAVE: where the waves' sums meet; SUMS: where each lane has its own
+    extern __shared__ __align__(16) float comb[];
+    constexpr bool SUMS = THREADS == 1024 && V == 2;
     const ep_block_norm_t& a = L.in;
     const int lane = WAVE ? threadIdx.x % kWave : threadIdx.x, lanes = WAVE ? kWave : blockDim.x;
     const int H = a.width, vecs = H / 8;
@@ -407,12 +418,36 @@ __global__ __launch_bounds__(THREADS) void block_norm_backward_kernel(BlockNormB
         fetch(first);
     if constexpr (KEEP)
         factors.keep(a, f);
-    float P[V][8], S[V][8];
+    float P[SUMS ? 1 : V][8], S[SUMS ? 1 : V][8];
 #pragma unroll
     for (int i = 0; i < V; ++i)
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            P[i][j] = S[i][j] = 0.0f;
+        for (int j = 0; j < 8; ++j) {
+            P[SUMS ? 0 : i][j] = S[SUMS ? 0 : i][j] = 0.0f;
+            if (SUMS && L.part && on[i])
+                comb[(lane + i * lanes) * 8 + j] = comb[H + (lane + i * lanes) * 8 + j] = 0.0f;
+        }
+    // adds a b to a lane's sums of its vector i, P (which = 0) or S
+    const auto add = [&](float (&kept)[SUMS ? 1 : V][8], int which, int i, const float (&a)[8], const float (&b)[8]) {
+        if constexpr (SUMS) {
+            if (L.part && on[i]) {
+                float4* c = reinterpret_cast<float4*>(comb + which * H + (lane + i * lanes) * 8);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    float4 v = c[k];
+                    v.x = __builtin_fmaf(a[4 * k], b[4 * k], v.x);
+                    v.y = __builtin_fmaf(a[4 * k + 1], b[4 * k + 1], v.y);
+                    v.z = __builtin_fmaf(a[4 * k + 2], b[4 * k + 2], v.z);
+                    v.w = __builtin_fmaf(a[4 * k + 3], b[4 * k + 3], v.w);
+                    c[k] = v;
+                }
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                kept[i][j] = __builtin_fmaf(a[j], b[j], kept[i][j]);
+        }
+    };
     for (int64_t row = first; row < a.num_rows; row += teams) {
         if (!KEEP)
             fetch(row);
@@ -468,14 +503,15 @@ __global__ __launch_bounds__(THREADS) void block_norm_backward_kernel(BlockNormB
             const float k = r * ss[1] * inv;
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                float fw[8];
+                float fw[8], gv[8], xh[8];
                 factors.get_w(a, i, lane + i * lanes, on[i], fw);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const float xh = v[i][j] * r;
-                    P[i][j] = __builtin_fmaf(gh[i].get(j), xh, P[i][j]);
-                    g[i][j] = __builtin_fmaf(r, gh[i].get(j) * fw[j] - xh * k, g[i][j]);
+                    gv[j] = gh[i].get(j);
+                    xh[j] = v[i][j] * r;
+                    g[i][j] = __builtin_fmaf(r, gv[j] * fw[j] - xh[j] * k, g[i][j]);
                 }
+                add(P, 0, i, gv, xh);
             }
         }
         if (L.dx) {
@@ -494,15 +530,16 @@ __global__ __launch_bounds__(THREADS) void block_norm_backward_kernel(BlockNormB
         float ss[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            float fy[8];
+            float fy[8], gv[8], z[8];
             factors.get_y(a, i, lane + i * lanes, on[i], fy);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const float z = y[i].get(j) * rz;
-                S[i][j] = __builtin_fmaf(gt * g[i][j], z, S[i][j]);
+                z[j] = y[i].get(j) * rz;
+                gv[j] = gt * g[i][j];
                 g[i][j] *= fy[j];
-                ss[0] = __builtin_fmaf(g[i][j], z, ss[0]);
+                ss[0] = __builtin_fmaf(g[i][j], z[j], ss[0]);
             }
+            add(S, 1, i, gv, z);
         }
         if (a.y_norm || (L.dgate && a.gate_kind == EP_GATE_TOKEN))
             sum(ss);
@@ -540,6 +577,10 @@ __global__ __launch_bounds__(THREADS) void block_norm_backward_kernel(BlockNormB
         }
         for (int c = threadIdx.x; c < 2 * H; c += THREADS)
             part[c] = comb[c];
+    } else if constexpr (SUMS) {
+        __syncthreads();
+        for (int c = threadIdx.x * 4; c < 2 * H; c += lanes * 4)
+            *reinterpret_cast<float4*>(part + c) = *reinterpret_cast<const float4*>(comb + c);
     } else {
 #pragma unroll
         for (int i = 0; i < V; ++i)
@@ -600,9 +641,15 @@ __global__ __launch_bounds__(kReduceThreads) void block_norm_reduce_kernel(Block
                     a.y_weight ? v * (a.weight_offset + load_param(a.y_weight, a.weights_f32, c)) : v);
 }
 
-// The team of a row and the workgroups: a wave with one or two vectors of eight a lane
-// up to a width of 1024, else a workgroup with one vector up to 2048, two up to
-// 16384, then four.
+// The team of a row: a wave with one or two vectors of eight a lane up to a width of
+// 1024, else a workgroup with one vector up to 2048, two up to 16384, then four.  In us
+// (16384 rows, bf16; forward, backward):
+//   1024: wave 26, 50; workgroup 33, 80      2048: one vector 52, 98; two 67, 105
+//   4096 (8192 rows): two vectors 50, 88; one 51, 114
+// From 8200 on a workgroup has up to 16 waves of 128 registers: factors are read again
+// (L2) and the next row is not fetched ahead.  4096 x 16384 takes 141 us forward, 323
+// backward (8 waves with four vectors each: 147, 388).  Beyond 16384 the backward pass
+// spills: 946 us for 2048 x 32768, 0.85 TB/s.
 struct Team {
     bool wave;
     int v, threads;
@@ -611,8 +658,12 @@ struct Team {
         const int64_t need = wave ? ((int64_t)rows + 3) / 4 : rows;
         return (int)(need < most ? need : most);
     }
-    // backward: as many workgroups as a CU holds at once (eight waves of 200 registers)
-    int backward_blocks(int rows) const { return blocks(rows, kCus * (threads <= 256 ? 2 : 1)); }
+    // Workgroups a CU takes at once.  Forward, in us: 16384 x 4096 92 with two, 133 with one, 99 with four; 8191 x 2056
+    // (three waves) 40 with two, 31 with four.  Backward (waves of 120 registers with one vector, 210 with two):
+    // 16384 x 2048 87 with three, 98 with two; 16384 x 1024 50 with two, 59 with four; 8192 x 4096 88 with two, 112
+    // with one
+    int forward_blocks(int rows) const { return blocks(rows, kCus * (v == 1 || wave || threads <= 192 ? 4 : 2)); }
+    int backward_blocks(int rows) const { return blocks(rows, kCus * (!wave && v == 1 ? 3 : threads <= 256 ? 2 : 1)); }
 };
 
 static Team team_of(int width)
@@ -650,7 +701,7 @@ struct Forward {
     static auto get() { return block_norm_kernel<WAVE, V, F32, THREADS, false>; }
 };
 template <bool WAVE, int V, bool F32, int THREADS>
-struct ForwardLarge {
+struct ForwardAround {
     static auto get() { return block_norm_kernel<WAVE, V, F32, THREADS, true>; }
 };
 template <bool WAVE, int V, bool F32, int THREADS>
@@ -663,11 +714,15 @@ hipError_t launch_block_norm(const BlockNormLaunch& L, hipStream_t stream)
     if (L.in.num_rows == 0)
         return hipSuccess;
     const Team t = team_of(L.in.width);
-    const int blocks = t.blocks(L.in.num_rows, kCus * (t.v == 1 || t.wave ? 4 : 2));
-    // outputs that do not stay in the Infinity Cache anyway pass it by
+    const int blocks = t.forward_blocks(L.in.num_rows);
+    // Outputs up to 16 MB are written through, which leaves less to write back at the kernel's end, and so are those that
+    // the Infinity Cache cannot hold (256 MB).  In between, who reads them next finds them there.  With bf16 x' and h,
+    // both read again by the next two calls, all of it in us, stores around the caches and through them:
+    //   512 x 7168   26.7, 28.5     1024 x 4096  25.8, 27.3     1024 x 7168  33.1, 31.6
+    //   8192 x 4096  97.0, 84.3     8192 x 7168   165, 158     16384 x 7168   309, 318
     const int64_t bytes = (int64_t)L.in.num_rows * L.in.width * ((L.xo ? L.in.x_f32 ? 4 : 2 : 0) + (L.h ? 2 : 0));
-    if (bytes > kLargeBytes)
-        return run_team<BlockNormLaunch, ForwardLarge>("block_norm", t, L, blocks, 0, stream);
+    if (bytes <= kSmallBytes || bytes > kLargeBytes)
+        return run_team<BlockNormLaunch, ForwardAround>("block_norm", t, L, blocks, 0, stream);
     return run_team<BlockNormLaunch, Forward>("block_norm", t, L, blocks, 0, stream);
 }
 
@@ -682,7 +737,8 @@ hipError_t launch_block_norm_backward(const BlockNormBackwardLaunch& L, hipStrea
     const Team t = team_of(L.in.width);
     const int blocks = t.backward_blocks(L.in.num_rows);
     if (blocks) {
-        const size_t lds = t.wave && L.part ? (size_t)2 * L.in.width * sizeof(float) : 0;
+        const bool sums = t.wave || (t.v == 2 && t.threads > 512);
+        const size_t lds = sums && L.part ? (size_t)2 * L.in.width * sizeof(float) : 0;
         const hipError_t e = run_team<BlockNormBackwardLaunch, Backward>("block_norm_backward", t, L, blocks, lds, stream);
         if (e != hipSuccess)
             return e;
