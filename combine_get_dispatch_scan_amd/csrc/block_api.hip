@@ -147,9 +147,9 @@ static int check_fp4(int w_f32, const char* flag, int num_groups, int n, int k)
     EP_TRY(check_width("k", k));
     if (num_groups < 1 || num_groups > EP_MAX_EXPERTS)
         return fail(EP_EINVAL, "num_groups=%d must be in [1, %d]", num_groups, EP_MAX_EXPERTS);
-    // eight weights a thread, four times, and fewer than 2^32 threads in a launch
-    if ((int64_t)n * k > ((int64_t)1 << 36) / num_groups)
-        return fail(EP_EINVAL, "%d groups of %d x %d weights are more than 2^36 in one call", num_groups, n, k);
+    // a launch has fewer than 2^32 threads, of 16 weights each
+    if ((int64_t)num_groups * n * k > (int64_t)1 << 35)
+        return fail(EP_EINVAL, "%d groups of %d x %d weights are more than 2^35 in one call", num_groups, n, k);
     return check_flag(flag, w_f32);
 }
 

@@ -732,7 +732,8 @@ int ep_block_norm_backward(const ep_block_norm_t* args, const void* grad_x, cons
  *   scales  device uint8 [G][N][K/32]
  * ep_dequantize_weights_fp4 writes code * scale as bf16 or (out_f32) fp32 [G][N][K],
  * exactly (2^128 and more, which a weight above 7/8 of that rounds to, is infinite).
- * All arrays 16-byte aligned, scales 4-byte.  Errors: EP_EINVAL, EP_EHIP.
+ * All arrays 16-byte aligned, scales 4-byte; at most 2^35 weights in a call.
+ * Errors: EP_EINVAL, EP_EHIP.
  */
 int ep_quantize_weights_fp4(const void* w, int w_f32, int num_groups, int n, int k, void* codes,
                             void* scales, hipStream_t stream);

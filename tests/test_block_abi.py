@@ -111,8 +111,8 @@ GEMM = dict(x=FAKE, x_scales=FAKE, scale_ld=0, w=FAKE, w_scales=FAKE, group_offs
     ("ep_quantize_weights_fp4", WEIGHTS, dict(w_f32=2), "w_f32"), ("ep_quantize_weights_fp4", WEIGHTS, dict(w=None), "w must"),
     ("ep_quantize_weights_fp4", WEIGHTS, dict(codes=FAKE + 8), "codes must"),
     ("ep_quantize_weights_fp4", WEIGHTS, dict(scales=FAKE + 1), "scales must"),
-    ("ep_quantize_weights_fp4", WEIGHTS, dict(num_groups=65, n=32768, k=32768), "2^36"),
-    ("ep_dequantize_weights_fp4", BACK, dict(num_groups=1024, n=32768, k=32768), "2^36"),
+    ("ep_quantize_weights_fp4", WEIGHTS, dict(num_groups=33, n=32768, k=32768), "2^35"),
+    ("ep_dequantize_weights_fp4", BACK, dict(num_groups=1024, n=32768, k=32768), "2^35"),
     ("ep_dequantize_weights_fp4", BACK, dict(k=0), "k=0"), ("ep_dequantize_weights_fp4", BACK, dict(out_f32=-1), "out_f32"),
     ("ep_dequantize_weights_fp4", BACK, dict(out=FAKE + 2), "out must"),
     ("ep_dequantize_weights_fp4", BACK, dict(codes=None), "codes must"),

@@ -345,6 +345,18 @@ def test_block_norm_gradient_of_the_norms_against_differences(ep):
         assert abs(got - want) <= step * size + 1e-6 * abs(want), (name, got, want)
 
 
+@pytest.mark.parametrize("T,H", [(3000, 4096), (9500, 7168)])
+def test_block_norm_of_many_rows_is_that_of_few(ep, T, H):
+    """Outputs of 49 and 272 MB are stored in other ways than those of up to 16 MB; a row's bits do not depend on it."""
+    o = _norm_case(12, T, H)
+    n = ep.block_norm(quantize=True, **o)
+    for a in (0, 1000, T - 500):
+        part = slice(a, a + 500)
+        m = ep.block_norm(quantize=True, **dict(o, **{k: o[k][part] for k in ("x", "y", "gate")}))
+        for k in ("x", "h", "codes", "scales"):
+            assert torch.equal(getattr(n, k)[part].view(torch.uint8), getattr(m, k).view(torch.uint8)), (a, k)
+
+
 def test_block_norm_binding_refusals(ep):
     dev = _dev()
     x = torch.zeros(4, 256, dtype=BF, device=dev)
@@ -466,6 +478,19 @@ def test_quantize_fp4_nan_and_infinity(ep):
     y = ep.grouped_gemm_fp4(x, xs, q.codes, q.scales, off)
     cols = torch.isnan(y).any(0)
     assert cols[[5, 7]].all() and int(cols.sum()) == 2 and torch.isnan(y[:, [5, 7]]).all()
+
+
+@pytest.mark.parametrize("G,N,K,dtype", [(4, 8192, 4224, BF), (8, 4096, 2304, torch.float32)])
+def test_quantize_fp4_of_many_weights_is_that_of_few(ep, G, N, K, dtype):
+    """Weights or results of more than 256 MB are read and stored in another way."""
+    w = torch.randn((G, N, K), generator=_gen(5), device=_dev(), dtype=dtype)
+    q = ep.quantize_weights_fp4(w)
+    for i in range(G):
+        p = ep.quantize_weights_fp4(w[i:i + 1])
+        assert torch.equal(q.codes[i], p.codes[0]) and torch.equal(q.scales[i].view(torch.uint8), p.scales[0].view(torch.uint8))
+    v = ep.dequantize_weights_fp4(q, dtype)
+    for i in range(G):
+        assert torch.equal(v[i], ep.dequantize_weights_fp4(ep.Fp4Weights(q.codes[i:i + 1], q.scales[i:i + 1]), dtype)[0])
 
 
 def _fp8_rows(g, rows, K, column_major=False):
