@@ -140,6 +140,13 @@ __global__ __launch_bounds__(kStreamWaves* kWave) void gemm_fp4_stream_kernel(Ge
 // The column of column tile c, from column tile 0's.
 __device__ __forceinline__ int column_step(int c) { return 32 * (c >> 1) + 4 * (c & 1); }
 
+// The column whose scales lie in place i in LDS: a column tile's sixteen follow each other,
+// so that lanes read 256 neighbouring bytes (or 64, one block apart from the next).
+__device__ __forceinline__ int scale_column(int i)
+{
+    return (i & ~31) | ((i & 12) << 1) | ((i >> 2) & 4) | (i & 3);
+}
+
 // A tile of WR x WC waves of (16 RT) x (16 CT) each, two K blocks at a time (256 bytes of a
 // row, 128 of a column) from LDS while the next two are copied in behind them.  Its last
 // barrier lies behind every read of LDS.
@@ -156,7 +163,7 @@ __device__ __forceinline__ void pair_tile(const GemmFp4Launch& a, int g, int m0,
     const int xrow = row0 + (lane & 15), col = column_of(col0, 0, lane);
     const int xbase = xrow * 2 * kQBlock + ((q ^ (lane & 7)) << 4);
     const int wbase = col * kQBlock + ((q ^ place_w(col)) << 4);
-    const int wsbase = col * (FOUR ? 16 : 4) + q;
+    const int wsbase = (col0 + (lane & 15)) * (FOUR ? 16 : 4) + q;
     const bool four = !a.x_scale_ld && KB % 4 == 0 && reinterpret_cast<uintptr_t>(a.x_scales) % 16 == 0;
     const int last_row = end - 1 - m0, last_col = N - 1 - n0;     // past the ends: the last one again
     const uint8_t* xp = a.x + (size_t)m0 * K;
@@ -203,7 +210,7 @@ __device__ __forceinline__ void pair_tile(const GemmFp4Launch& a, int g, int m0,
             }
         } else if (wave < ROWS / 64 + COLS / 64) {
             const int part = wave - ROWS / 64;
-            const uint32_t o = min(part * 64 + lane, last_col) * (uint32_t)(K / 32);
+            const uint32_t o = min(scale_column(part * 64 + lane), last_col) * (uint32_t)(K / 32);
             if (FOUR) {
                 load_to_lds16(wsp + (o + kb * 4), sw + part * 1024);
             } else {
@@ -238,7 +245,7 @@ __device__ __forceinline__ void pair_tile(const GemmFp4Launch& a, int g, int m0,
                 s[h][r] = f[(four ? 64 : 16) * r];
 #pragma unroll
             for (int c = 0; c < CT; ++c)
-                ws[h][c] = u[column_step(c) * (FOUR ? 16 : 4)];
+                ws[h][c] = u[16 * c * (FOUR ? 16 : 4)];
         }
         if (p + 1 < pairs) {
             copy(p + 1, nx, nw);
@@ -403,7 +410,7 @@ __global__ __launch_bounds__(512, 2) void gemm_fp4_tile_kernel(GemmFp4Launch a)
     const int xbase = (row0 + (lane & 15)) * kQBlock + (((lane >> 4) ^ place_x(lane & 15)) << 4);
     const int col = column_of(col0, 0, lane);
     const int wbase = col * kQBlock + (((lane >> 4) ^ place_w(col)) << 4);
-    const int wsbase = col * (FOUR ? 16 : 4) + (lane >> 4);
+    const int wsbase = (col0 + (lane & 15)) * (FOUR ? 16 : 4) + (lane >> 4);
     const int64_t t0 = (int64_t)(blockIdx.x % kXcds) * (gridDim.x / kXcds) + blockIdx.x / kXcds;
     // Where three CUs of four or more would be idle in the last round, its tiles are split into four of 128 x 128
     // (512 rows a group, 640 in some, 4096 x 7168: 470 us for 1088 tiles, 492 without; 530 for 1312, 556 without).
@@ -457,7 +464,7 @@ __global__ __launch_bounds__(512, 2) void gemm_fp4_tile_kernel(GemmFp4Launch a)
             src.so = a.x_scale_ld ? min(r, last_row) : (uint32_t)min(r, last_row) * KB;
             src.sld = a.x_scale_ld;
             src.four = !a.x_scale_ld && KB % 4 == 0 && reinterpret_cast<uintptr_t>(a.x_scales) % 16 == 0;
-            src.wso = (uint32_t)min(r, last_col) * (K / 32);
+            src.wso = (uint32_t)min(scale_column(r), last_col) * (K / 32);
         }
         const bool on = row0 <= last_row && col0 <= last_col;
         f32x4 acc[4][8];
@@ -487,7 +494,7 @@ __global__ __launch_bounds__(512, 2) void gemm_fp4_tile_kernel(GemmFp4Launch a)
             const uint8_t* q = lws[(kb >> 2) & 1] + wsbase + (kb & 3) * (FOUR ? 4 : 1024);
 #pragma unroll
             for (int c = 0; c < 8; ++c)
-                ws[c] = q[column_step(c) * (FOUR ? 16 : 4)];
+                ws[c] = q[16 * c * (FOUR ? 16 : 4)];
             if (kb + 1 < KB) {
                 copy_x(src, kb + 1, wave, nx);
                 if ((kb + 1) % 4 == 0) {
