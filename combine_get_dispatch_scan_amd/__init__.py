@@ -13,7 +13,8 @@ Two layers:
   ``dispatch_backward`` / ``combine_backward`` / ``handle_recv_counts`` -- the
   same calls on torch tensors: they allocate
   the outputs with ``torch.empty`` on the tensors' device and launch on torch's
-  current stream.
+  current stream.  The expert layer's calls (``gate`` ... ``swiglu_fp8``) are those of
+  ``experts``, the norms around it and 4-bit weights those of ``block``.
 """
 from __future__ import annotations
 

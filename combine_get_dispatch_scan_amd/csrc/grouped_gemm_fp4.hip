@@ -540,7 +540,7 @@ __global__ __launch_bounds__(512, 2) void gemm_fp4_tile_kernel(GemmFp4Launch a)
 
 // Small tiles, 64 rows x 128 columns by four waves of 32 x 64 each; two workgroups a CU, so
 // that one computes while the other waits.  256 rows in 32 groups, 4096 x 7168: 92 us,
-// 5.5 TB/s (HBM); 4096 rows in 64 groups with zipf popularity, 2816 x 2048: 66 us (two
+// 5.5 TB/s (HBM); 4096 rows in 64 groups with zipf popularity, 2816 x 2048: 66 us (4.6
 // rounds of tiles, 0.71 PFLOP/s).
 constexpr int kSmallRows = 64, kSmallCols = 128;
 
