@@ -100,12 +100,9 @@ def ep_grouped_gemm_fp4(x, x_scales, scale_ld, w, w_scales, group_offsets, num_g
 
 def _rows(t, T, H, name):
     """Elements between the rows of a matrix [T, H] whose rows are contiguous (they may lie apart)."""
-    if t.is_contiguous():
-        ld, step = H, 1
-    else:
-        ld, step = t.stride()
-        if T <= 1:
-            ld = H
+    ld, step = (H, 1) if t.is_contiguous() else t.stride()
+    if T <= 1:
+        ld = H
     if step != 1 and T > 0 and H > 1:
         raise ValueError(f"the rows of {name} must be contiguous")
     if ld < H or ld % 8:
@@ -125,14 +122,16 @@ def _f32(t, name):
 
 def _norm_args(x, y, norm, weight, y_norm, y_weight, gate, residual_scale, y_scale, eps, weight_offset):
     import torch
-    T, H = _matrix(x, "x")
-    _i32(H, "width")
+    T, H = shape = _matrix(x, "x")
+    if H >= 2 ** 31:
+        _i32(H, "width")
     yp = wp = ywp = gp = None
     y_ld = weights_f32 = kind = gate_f32 = 0
     x_f32 = _f32(x, "x")
     x_ld = _rows(x, T, H, "x")
     if y is not None:
-        _shape(y, (T, H), "y")
+        if y.shape != shape:
+            _shape(y, (T, H), "y")
         if y.dtype is not torch.bfloat16:
             raise TypeError(f"y must be torch.bfloat16, got {y.dtype}")
         yp, y_ld = y.data_ptr(), _rows(y, T, H, "y")
@@ -163,6 +162,8 @@ def _norm_args(x, y, norm, weight, y_norm, y_weight, gate, residual_scale, y_sca
 def _empty(t, dtype=None):
     """A dense tensor of t's shape (empty_like costs the host two thirds of what empty does)."""
     import torch
+    if dtype is None and t.is_contiguous():
+        return torch.empty_like(t)
     return torch.empty_like(t, dtype=dtype, memory_format=torch.contiguous_format)
 
 
@@ -214,10 +215,10 @@ def block_norm(x, y=None, *, norm: bool = True, weight=None, y_norm: bool = Fals
             x_out = _empty(x)
         h = codes = scales = None
         if norm and write_h:
-            h = _empty(x, torch.bfloat16)
+            h = _empty(x, None if x.dtype is torch.bfloat16 else torch.bfloat16)
         if quantize:
             codes = _empty(x, torch.float8_e4m3fn)
-            scales = torch.empty((T, H // 128), dtype=torch.float32, device=x.device)
+            scales = torch.empty_strided((T, H // 128), (H // 128, 1), dtype=torch.float32, device=x.device)
         _check(ep_block_norm(a, _ptr(x_out, None, "x_out"), _at(h), _at(codes) if T else None,
                              _at(scales) if T else None, _stream(x)))
     return BlockNorm(x if y is None else x_out, h, codes, scales)
@@ -303,7 +304,7 @@ def quantize_weights_fp4(w) -> Fp4Weights:
     with _on(w):
         codes = torch.empty((G, N, K // 2), dtype=torch.uint8, device=w.device)
         scales = torch.empty((G, N, K // 32), dtype=torch.float8_e8m0fnu, device=w.device)
-        _check(ep_quantize_weights_fp4(_ptr(w, name="w"), f32, _i32(G, "G"), N, K, _ptr(codes), _ptr(scales),
+        _check(ep_quantize_weights_fp4(_ptr(w, name="w"), f32, _i32(G, "G"), N, K, _at(codes), _at(scales),
                                        _stream(w)))
     return Fp4Weights(codes, scales)
 
@@ -311,9 +312,11 @@ def quantize_weights_fp4(w) -> Fp4Weights:
 def _fp4_shape(w, w_scales):
     if w.dim() != 3:
         raise ValueError(f"w must be [G, N, K/2], got shape {list(w.shape)}")
-    G, N, K = w.shape[0], w.shape[1], 2 * w.shape[2]
-    _width(N, "N")
-    _width(K, "K")
+    G, N, K = w.shape
+    K *= 2
+    if N % 128 or K % 128 or not (0 < N < 2 ** 31 and 0 < K < 2 ** 31):
+        _width(N, "N")
+        _width(K, "K")
     _shape(w_scales, (G, N, K // 32), "w_scales")
     return G, N, K
 
@@ -327,7 +330,7 @@ def dequantize_weights_fp4(w: Fp4Weights, dtype=None):
         out = torch.empty((G, N, K), dtype=dtype or torch.bfloat16, device=w.codes.device)
         f32 = _f32(out, "dtype")
         _check(ep_dequantize_weights_fp4(_ptr(w.codes, "fp4", "codes"), _ptr(w.scales, "e8m0", "scales"),
-                                         _i32(G, "G"), N, K, _ptr(out), f32, _stream(out)))
+                                         _i32(G, "G"), N, K, _at(out), f32, _stream(out)))
     return out
 
 
@@ -338,19 +341,20 @@ def grouped_gemm_fp4(x, x_scales, w, w_scales, groups, *, group_stride: int = 0,
     out[r] = x[r] @ w[g].T for the rows r of group g, bf16 [rows, N]."""
     import torch
     rows, K = _matrix(x, "x")
-    _width(K, "K")
     G, N, k = _fp4_shape(w, w_scales)
     if k != K:
         raise ValueError(f"w must be [G, N, {K // 2}], got shape {list(w.shape)}")
     ld = _row_scales(x_scales, rows, K, column_major_scales, "x_scales")
-    group_stride, expected_rows = _i32(group_stride, "group_stride"), _i32(expected_rows, "expected_rows")
+    if group_stride or expected_rows:
+        group_stride, expected_rows = _i32(group_stride, "group_stride"), _i32(expected_rows, "expected_rows")
     with _on(x, x_scales, w, w_scales, out):
         args, expected = _group_args(groups, group_stride, x)
         if args[1] != G:
             raise ValueError(f"w holds {G} groups, the rows {args[1]}")
         if out is None:
             out = torch.empty((rows, N), dtype=torch.bfloat16, device=x.device)
-        _shape(out, (rows, N), "out")
+        elif out.shape != (rows, N):
+            _shape(out, (rows, N), "out")
         _check(ep_grouped_gemm_fp4(_ptr(x, "fp8", "x"), _ptr(x_scales, "f32", "x_scales"), ld,
                                    _ptr(w, "fp4", "w"), _ptr(w_scales, "e8m0", "w_scales"), *args, rows, N, K,
                                    expected_rows or expected, _ptr(out, "bf16", "out"), _stream(x)))
