@@ -165,7 +165,7 @@ __device__ __forceinline__ void pair_tile(const GemmFp4Launch& a, int g, int m0,
     const int wbase = col * kQBlock + ((q ^ place_w(col)) << 4);
     const int wsbase = (col0 + (lane & 15)) * (FOUR ? 16 : 4) + q;
     const bool four = !a.x_scale_ld && KB % 4 == 0 && reinterpret_cast<uintptr_t>(a.x_scales) % 16 == 0;
-    const int last_row = end - 1 - m0, last_col = N - 1 - n0;     // past the ends: the last one again
+    const int last_row = __builtin_amdgcn_readfirstlane(end - 1 - m0), last_col = N - 1 - n0;
     const uint8_t* xp = a.x + (size_t)m0 * K;
     const uint8_t* wp = a.w + ((size_t)g * N + n0) * (K / 2);
     const uint8_t* wsp = a.w_scales + ((size_t)g * N + n0) * (K / 32);
@@ -185,13 +185,15 @@ __device__ __forceinline__ void pair_tile(const GemmFp4Launch& a, int g, int m0,
     // high bits: none of x's, bit 0 of the wave of w's)
     const int xtail = (KB & 1) && (lane & 8) ? kQBlock : 0;
     const int wtail = (KB & 1) && (((lane >> 2) ^ wave) & 1) ? kQBlock / 2 : 0;
+    // copies with no row of the group are left out (what LDS holds there only reaches rows that are not stored): 256 rows
+    // in 32 groups, 90 us, 92 with them.  In the others, rows and columns past the ends are the last one again
     const auto copy = [&](int p, uint8_t* lx, uint8_t* lw) {
         const bool last = p == pairs - 1;
 #pragma unroll
         for (int j = 0; j < (XC > WCP ? XC : WCP); ++j) {
             if (j < WCP)
                 load_to_lds16(wp + (wo[j < WCP ? j : 0] + p * kQBlock - (last ? wtail : 0)), lw + (WAVES * j + wave) * 1024);
-            if (j < XC)
+            if (j < XC && (WAVES * j + wave) * 4 <= last_row)
                 load_to_lds16(xp + (xo[j < XC ? j : 0] + p * 2 * kQBlock - (last ? xtail : 0)), lx + (WAVES * j + wave) * 1024);
         }
     };
@@ -539,9 +541,10 @@ __global__ __launch_bounds__(512, 2) void gemm_fp4_tile_kernel(GemmFp4Launch a)
 }
 
 // Small tiles, 64 rows x 128 columns by four waves of 32 x 64 each; two workgroups a CU, so
-// that one computes while the other waits.  256 rows in 32 groups, 4096 x 7168: 92 us,
-// 5.5 TB/s (HBM); 4096 rows in 64 groups with zipf popularity, 2816 x 2048: 66 us (4.6
-// rounds of tiles, 0.71 PFLOP/s).
+// that one computes while the other waits.  256 rows in 32 groups, 4096 x 7168: 90 us,
+// 5.6 TB/s (HBM); 4096 rows in 64 groups with zipf popularity, 2816 x 2048: 66 us (4.6
+// rounds of tiles, 0.71 PFLOP/s).  A ring of four single blocks, three on their way, was
+// slower (103 and 72 us): 64-byte pieces of columns, twice the barriers.
 constexpr int kSmallRows = 64, kSmallCols = 128;
 
 template <bool FOUR>
