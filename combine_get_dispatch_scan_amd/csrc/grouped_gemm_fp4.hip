@@ -617,9 +617,9 @@ static void tile_run(const GemmFp4Launch& L, hipStream_t stream)
 // The form by the typical rows m of a group.  32 groups, N = 4096, K = 7168 (499 MB of
 // weights and scales; 98 us at the rate of a large copy), in us, rows falling evenly:
 //   rows in all     8     64    128    256    512   1024   2048   4096   8192  16384
-//   streamed       26     82     92     98    130    211
-//   small          34     85     90     92     95    104    151    217    366    710
-//   large          71    143    146    146    146    148    160    195    333    527
+//   streamed       24     81     91     99    138    215
+//   small          31     84     88     91     94    103    142    209    345    644
+//   large          68    143    145    146    146    149    155    184    299    488
 // (8 rows: eight groups of one.)  Beyond such full cards it is how many tiles there are
 // that counts: a form's time is that of its rounds over the card, and a round costs
 // nearly the same however few tiles are in it (but the large form's last one, if its
@@ -647,7 +647,7 @@ hipError_t launch_grouped_gemm_fp4(const GemmFp4Launch& L, hipStream_t stream)
     if (KB <= kStreamWaves * B) {
         const int64_t room = kCus * (kStreamWaves / ((KB + B - 1) / B)), rounds = (tiles(16, kStreamCols) + room - 1) / room;
         const int64_t time = 800 + rounds * (250 + 20 * KB);
-        // at one or two rows a group its lead is small, but the model does not see it (82 us against 85 above)
+        // at one or two rows a group its lead is small, but the model does not see it (81 us against 84 above)
         if (m <= 2 || ((m <= 16 || rounds == 1) && time < small_time && time < large_time)) {
             B == 4 ? stream_run<4>(L, stream) : stream_run<8>(L, stream);
             return hipGetLastError();
