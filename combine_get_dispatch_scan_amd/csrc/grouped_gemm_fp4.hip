@@ -628,7 +628,7 @@ static void tile_run(const GemmFp4Launch& L, hipStream_t stream)
 //   small     8.0 + KB * max(0.75, tiles / 650)
 //   large     7.5 + rounds * (2 + 1.55 KB), of which 2 + KB for a split round    (us)
 // which was fitted to 393 shapes (1 to 64 groups, m = 1 to 4096, N and K up to 8192, even,
-// equal and zipf rows).  There this choice takes 1.4 % longer than the best form.
+// equal and zipf rows).  There this choice takes 1.3 % longer than the best form.
 hipError_t launch_grouped_gemm_fp4(const GemmFp4Launch& L, hipStream_t stream)
 {
     if (L.groups.rows == 0 || L.groups.num == 0)
@@ -647,8 +647,9 @@ hipError_t launch_grouped_gemm_fp4(const GemmFp4Launch& L, hipStream_t stream)
     if (KB <= kStreamWaves * B) {
         const int64_t room = kCus * (kStreamWaves / ((KB + B - 1) / B)), rounds = (tiles(16, kStreamCols) + room - 1) / room;
         const int64_t time = 800 + rounds * (250 + 20 * KB);
-        // at one or two rows a group its lead is small, but the model does not see it (81 us against 84 above)
-        if (m <= 2 || ((m <= 16 || rounds == 1) && time < small_time && time < large_time)) {
+        // at one or two rows a group its lead is small, but the model does not see it (81 us against 84 above); two
+        // blocks of K are too few for it (27 groups of two rows, 7680 x 256: 15.5 us, small 10.2)
+        if ((m <= 2 && KB > 2) || ((m <= 16 || rounds == 1) && time < small_time && time < large_time)) {
             B == 4 ? stream_run<4>(L, stream) : stream_run<8>(L, stream);
             return hipGetLastError();
         }

@@ -227,7 +227,7 @@ import torch
 import combine_get_dispatch_scan_amd as ep
 g = torch.Generator(device="cuda")
 g.manual_seed(0)
-for G, rows, N, K in ((4, 4, 128, 256), (2, 2, 128, 8192), (2, 2, 128, 8320), (8, 4096, 512, 1024), (2, 16384, 2048, 512)):
+for G, rows, N, K in ((4, 4, 128, 256), (4, 4, 128, 384), (2, 2, 128, 8192), (2, 2, 128, 8320), (8, 4096, 512, 1024), (2, 16384, 2048, 512)):
     x = torch.randn(rows, K, generator=g, device="cuda").to(torch.float8_e4m3fn)
     w = ep.quantize_weights_fp4(torch.randn(G, N, K, generator=g, device="cuda"))
     off = torch.arange(0, rows + 1, rows // G, device="cuda", dtype=torch.int32)
@@ -250,7 +250,7 @@ def test_every_form_is_reached(ep):
     assert r.returncode == 0, r.stderr[-2000:]
     got = [l.split()[1] for l in r.stderr.splitlines() if l.startswith("[moe_ep]")]
     assert [n for n in got if n.startswith("grouped")] == ["grouped_gemm_fp4_" + n
-                                                           for n in ("stream", "stream", "small", "small", "tile")]
+                                                           for n in ("small", "stream", "stream", "small", "small", "tile")]
     threads = [int(l.split("block=(")[1].split(",")[0]) for l in r.stderr.splitlines() if l.startswith("[moe_ep] block_norm ")]
     assert threads == [256, 256, 1024]
     assert [n for n in got if n.startswith("block_norm")] == ["block_norm", "block_norm_backward", "block_norm_reduce"] * 3
