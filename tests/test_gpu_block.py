@@ -662,3 +662,55 @@ def test_fp4_offsets_outside_the_rows_are_clamped(ep, off, stride, expected):
             e = min(max(off[i + 1], b), rows)
         touched[b:e] = True
     assert torch.equal(out.ne(0).any(1).cpu(), touched)
+
+
+# ----------------------------------------------------------------------------
+# offsets past 32 bits
+# ----------------------------------------------------------------------------
+
+def test_block_norm_past_2_to_the_31_elements(ep):
+    """The last rows of 66000 x 32768 (and of a stride of 32776) equal a call on them alone."""
+    dev = _dev()
+    T, H = 66000, 32768
+    x = torch.zeros(T, H + 8, dtype=BF, device=dev)[:, :H]
+    y = torch.zeros(T, H, dtype=BF, device=dev)
+    last = slice(T - 4, T)
+    g = _gen(70)
+    x[last], y[last] = _randn(g, 4, H).to(BF), _randn(g, 4, H).to(BF)
+    w, gate = torch.randn(H, generator=g, device=dev), torch.ones(T, 1, device=dev)
+    o = dict(weight=w, y_norm=True, y_weight=w)
+    n = ep.block_norm(x, y, gate=gate, quantize=True, **o)
+    m = ep.block_norm(x[last], y[last], gate=gate[last], quantize=True, **o)
+    for k in ("x", "h", "codes", "scales"):
+        assert torch.equal(getattr(n, k)[last].view(torch.uint8), getattr(m, k).view(torch.uint8)), k
+        assert not getattr(n, k)[:8].float().isnan().any()
+    del n
+    q = ep.block_norm_backward(x, y, grad_x=y, grad_h=y, gate=gate, need=("x", "y", "gate"), **o)
+    p = ep.block_norm_backward(x[last], y[last], grad_x=y[last], grad_h=y[last], gate=gate[last], need=("x", "y", "gate"), **o)
+    for k in ("x", "y", "gate"):
+        assert torch.equal(getattr(q, k)[last], getattr(p, k)), k
+
+
+def test_fp4_past_2_to_the_31_elements(ep):
+    """Weights, codes, rows and outputs whose offsets pass 32 bits: the last group against a call on it alone."""
+    dev = _dev()
+    G, N, K = 9, 32768, 16384
+    w = torch.zeros(G, N, K, dtype=BF, device=dev)
+    w[-1] = torch.randn((N, K), generator=_gen(71), device=dev, dtype=BF)
+    q = ep.quantize_weights_fp4(w)
+    r = ep.quantize_weights_fp4(w[-1:])
+    del w
+    assert torch.equal(q.codes[-1], r.codes[0]) and torch.equal(q.scales[-1].view(torch.uint8), r.scales[0].view(torch.uint8))
+    assert torch.equal(ep.dequantize_weights_fp4(q)[-1], ep.dequantize_weights_fp4(r)[0])
+    rows = 140000
+    x = torch.zeros(rows, K, dtype=torch.uint8, device=dev).view(F8)
+    xs = torch.ones(rows, K // 128, device=dev)
+    x[-300:] = (_randn(_gen(72), 300, K) * 50).to(F8)
+    few = torch.tensor([0, 300], dtype=torch.int32, device=dev)
+    off = torch.full((G + 1,), rows - 300, dtype=torch.int32, device=dev)
+    off[0], off[-1] = rows - 301, rows
+    out = torch.empty(rows, N, dtype=BF, device=dev)
+    for expected in (40, 100000):
+        ep.grouped_gemm_fp4(x, xs, q.codes, q.scales, off, expected_rows=expected, out=out)
+        assert torch.equal(out[-300:], ep.grouped_gemm_fp4(x[-300:], xs[-300:], r.codes, r.scales, few, expected_rows=expected))
+        assert not out[-301].any()
