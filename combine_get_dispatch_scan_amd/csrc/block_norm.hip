@@ -74,6 +74,22 @@ struct TeamSum {
     }
 };
 
+// A row's mean square is sum((v * part) * v) * rest: part the largest power of two that is at most 1 / width, part * rest
+// = 1 / width.  The sum then stays in fp32's range wherever the mean does (the sum of the squares themselves left it from
+// values of 2^56.5 on at the largest width).  A power of two moves no rounding; only terms below 2^-126, which eps drowns,
+// lose bits.
+struct MeanSquare {
+    float part, rest;
+
+    __device__ __forceinline__ explicit MeanSquare(int width)
+    {
+        const int k = 32 - __clz(width - 1);              // 2^k: width, or the next power of two above it
+        part = __uint_as_float((uint32_t)(127 - k) << 23);
+        rest = 1.0f / (float)width * __uint_as_float((uint32_t)(127 + k) << 23);
+    }
+    __device__ __forceinline__ float add(float v, float sum) const { return __builtin_fmaf(v * part, v, sum); }
+};
+
 // Eight channels of a vector of parameters as they lie in memory (fp32, or bf16 twice).
 // Loading and widening are apart, so that all loads are on their way before one is waited for.
 struct RawParam8 {
@@ -235,7 +251,7 @@ __global__ __launch_bounds__(THREADS) void block_norm_kernel(BlockNormLaunch L)
     const int H = a.width, vecs = H / 8;
     const int teams = WAVE ? gridDim.x * (THREADS / kWave) : gridDim.x;
     const int first = WAVE ? blockIdx.x * (THREADS / kWave) + threadIdx.x / kWave : blockIdx.x;
-    const float inv = 1.0f / (float)H;
+    const MeanSquare square(H);
     TeamSum<WAVE, 1> sum{slots, 0};
     constexpr bool KEEP = THREADS <= 512;
     bool on[V];
@@ -289,9 +305,9 @@ __global__ __launch_bounds__(THREADS) void block_norm_kernel(BlockNormLaunch L)
                 for (int i = 0; i < V; ++i)
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
-                        ss[0] = __builtin_fmaf(y[i].get(j), y[i].get(j), ss[0]);
+                        ss[0] = square.add(y[i].get(j), ss[0]);
                 sum(ss);
-                cy = __builtin_amdgcn_rsqf(ss[0] * inv + a.eps);
+                cy = __builtin_amdgcn_rsqf(ss[0] * square.rest + a.eps);
             }
             if (a.gate_kind == EP_GATE_TOKEN)
                 cy *= load_param(a.gate, a.gate_f32, (int)row);
@@ -319,9 +335,9 @@ __global__ __launch_bounds__(THREADS) void block_norm_kernel(BlockNormLaunch L)
         for (int i = 0; i < V; ++i)
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                ss[0] = __builtin_fmaf(v[i][j], v[i][j], ss[0]);
+                ss[0] = square.add(v[i][j], ss[0]);
         sum(ss);
-        const float r = __builtin_amdgcn_rsqf(ss[0] * inv + a.eps);
+        const float r = __builtin_amdgcn_rsqf(ss[0] * square.rest + a.eps);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int vec = lane + i * lanes;
@@ -381,6 +397,7 @@ __global__ __launch_bounds__(THREADS) void block_norm_backward_kernel(BlockNormB
     const int teams = WAVE ? gridDim.x * (THREADS / kWave) : gridDim.x;
     const int first = WAVE ? blockIdx.x * (THREADS / kWave) + threadIdx.x / kWave : blockIdx.x;
     const float inv = 1.0f / (float)H;
+    const MeanSquare square(H);
     TeamSum<WAVE, 2> sum{slots, 0};
     constexpr bool KEEP = THREADS <= 512;
     bool on[V];
@@ -469,9 +486,9 @@ __global__ __launch_bounds__(THREADS) void block_norm_backward_kernel(BlockNormB
             for (int i = 0; i < V; ++i)
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                    ss[0] = __builtin_fmaf(y[i].get(j), y[i].get(j), ss[0]);
+                    ss[0] = square.add(y[i].get(j), ss[0]);
             sum(ss);
-            rz = __builtin_amdgcn_rsqf(ss[0] * inv + a.eps);
+            rz = __builtin_amdgcn_rsqf(ss[0] * square.rest + a.eps);
         }
         if (a.gate_kind == EP_GATE_TOKEN)
             gt = load_param(a.gate, a.gate_f32, (int)row);
@@ -494,12 +511,12 @@ __global__ __launch_bounds__(THREADS) void block_norm_backward_kernel(BlockNormB
                 for (int j = 0; j < 8; ++j) {
                     v[i][j] = a.y ? __builtin_fmaf(a.residual_scale, x[i].get(j), y[i].get(j) * cy * fy[j])
                                   : x[i].get(j);
-                    ss[0] = __builtin_fmaf(v[i][j], v[i][j], ss[0]);
+                    ss[0] = square.add(v[i][j], ss[0]);
                     ss[1] = __builtin_fmaf(gh[i].get(j) * fw[j], v[i][j], ss[1]);
                 }
             }
             sum(ss);
-            const float r = __builtin_amdgcn_rsqf(ss[0] * inv + a.eps);
+            const float r = __builtin_amdgcn_rsqf(ss[0] * square.rest + a.eps);
             const float k = r * ss[1] * inv;
 #pragma unroll
             for (int i = 0; i < V; ++i) {

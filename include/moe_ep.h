@@ -709,7 +709,8 @@ int ep_block_norm(const ep_block_norm_t* args, void* x_out, void* h, void* codes
  *   out_weight, out_y_weight   fp32 or bf16 like the weights, [width]
  *   out_gate       like the gate, [num_rows] or [width]
  * NULL outputs are not written; one is given.  Sums over rows are taken in an
- * order fixed by the sizes: results repeat bit for bit.
+ * order fixed by the sizes: results repeat bit for bit.  A row's sum of
+ * |grad_h * (weight_offset + weight) * x'| must stay in fp32's range.
  *   ws             ep_block_norm_workspace_bytes(num_rows, width) bytes, 256-byte
  *                  aligned, where out_weight, out_y_weight or a channel's out_gate is
  *                  given (else NULL); free again once the call's work has run
