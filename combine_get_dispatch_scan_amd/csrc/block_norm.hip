@@ -4,14 +4,16 @@
 //   h  = x' r (o + weight),  r = 1 / sqrt(mean x'^2 + eps),  as bf16 and as FP8 rows
 // and their gradients.  A team of lanes (a wave, or a workgroup of up to 16) holds a
 // row in registers, so every value is read and written once; means are fp32 sums
-// over the lanes.  All arithmetic is fp32, and every output is rounded once.
+// over the lanes.  All arithmetic is fp32, and every output is rounded once, by gfx950's
+// converter: a NaN of any bits stays one.
 //
 // Memory bounds both: 16384 x 7168 in bf16 with y's norm, weights, a token gate and 8-bit
-// rows takes 190 us forward, 5.6 TB/s (a copy of 1 GiB: 5.1), and 298 us backward, 4.7 TB/s.
+// rows takes 186 us forward, 5.7 TB/s (a copy of 1 GiB: 5.1), and 289 us backward, 4.9 TB/s.
 // To keep it busy a team fetches its next row before it computes the one it has, and
 // parameters are widened after all of them are on their way (with the wide loads of the
-// second launch: 298 us, 373 before).  One row takes 4.6 us, of which the launch is most.
+// second launch: 298 us, 373 without).  One row takes 4.3 us, of which the launch is most.
 #include "block_launch.h"
+#include "mfma.h"
 #include "quant16.h"
 
 namespace moe_ep {
@@ -121,7 +123,7 @@ __device__ __forceinline__ void store_param(void* p, bool f32, int i, float v)
     if (f32)
         static_cast<float*>(p)[i] = v;
     else
-        static_cast<uint16_t*>(p)[i] = (uint16_t)f32_to_bf16_rne(v);
+        static_cast<uint16_t*>(p)[i] = (uint16_t)pack2_bf16(v, v);
 }
 
 // The parameters of eight channels, and what they make up: y's factor and the norm's.
@@ -236,7 +238,7 @@ struct Raw8 {
             u32x4 o;
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                o[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
+                o[j] = pack2_bf16(v[2 * j], v[2 * j + 1]);
             store16_hint<NT>(q, o);
         }
     }
@@ -259,7 +261,20 @@ __global__ __launch_bounds__(THREADS) void block_norm_kernel(BlockNormLaunch L)
     Factors<V, KEEP> factors;
     Raw8<F32> nx[V];
     Raw8<false> ny[V];
-    // a row on its way while the one before it is computed
+    // a row on its way while the one before it is computed: y from its start, x from its second half on (16384 x 7168
+    // 186 us, 8192 x 4096 50; both from the start 198 and 51, both from the second half 191 and 59)
+    const auto fetch_y = [&](int64_t row) {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (on[i] && a.y)
+                ny[i].load(a.y, row * a.y_ld + (lane + i * lanes) * 8);
+    };
+    const auto fetch_x = [&](int64_t row) {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (on[i])
+                nx[i].load(a.x, row * a.x_ld + (lane + i * lanes) * 8);
+    };
     const auto fetch = [&](int64_t row) {
 #pragma unroll
         for (int i = 0; i < V; ++i)
@@ -295,7 +310,7 @@ __global__ __launch_bounds__(THREADS) void block_norm_kernel(BlockNormLaunch L)
             y[i] = ny[i];
         }
         if (KEEP && row + teams < a.num_rows)
-            fetch(row + teams);
+            fetch_y(row + teams);
         float v[V][8];
         float ss[1] = {0.0f};
         if (a.y) {
@@ -328,6 +343,8 @@ __global__ __launch_bounds__(THREADS) void block_norm_kernel(BlockNormLaunch L)
                 for (int j = 0; j < 8; ++j)
                     v[i][j] = x[i].get(j);
         }
+        if (KEEP && row + teams < a.num_rows)
+            fetch_x(row + teams);
         if (!a.norm)
             continue;
         ss[0] = 0.0f;

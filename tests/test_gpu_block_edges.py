@@ -33,3 +33,36 @@ def test_block_norm_of_large_values(ep, H, xt, gate):
     _check_norm(ep, o)
     _check_norm_backward(ep, o, H + 1)
     _check_norm(ep, dict(o, y=None, gate=None, residual_scale=1.0))
+
+
+# NaNs as arithmetic makes them, with every bit set (memory filled with 0xFF), and signalling
+@pytest.mark.parametrize("bits", [0x7FC00000, 0x7FFFFFFF, -1, 0x7FFF8000, 0x7F800001])
+@pytest.mark.parametrize("H", [256, 2048, 8320])
+def test_block_norm_keeps_every_nan(ep, bits, H):
+    """A NaN of any bits in the 32-bit stream, its gradient, a weight or a gate is a NaN in all outputs it reaches."""
+    def at(shape, *where):
+        t = _randn(g, *shape)
+        t.view(torch.int32)[where] = bits
+        return t
+
+    g = _gen(H)
+    x, y, w = _randn(g, 5, H), _randn(g, 5, H).to(BF), _randn(g, H)
+    bad = at((5, H), 2, 7)
+    live = [0, 1, 3, 4]
+    for n in (ep.block_norm(bad, quantize=True), ep.block_norm(bad, y, weight=w, quantize=True)):
+        assert torch.isnan(n.x[2, 7]) and int(torch.isnan(n.x).sum()) == 1
+        assert torch.isnan(n.h[2]).all() and torch.isnan(n.codes[2].float()).all()
+        assert torch.isfinite(n.h[live].float()).all() and torch.isfinite(n.codes[live].float()).all()
+    n = ep.block_norm(x, weight=at((H,), 9), quantize=True)
+    assert torch.isnan(n.h[:, 9]).all() and int(torch.isnan(n.h).sum()) == 5 and torch.isnan(n.codes[:, 9].float()).all()
+    n = ep.block_norm(x.to(BF), y, gate=at((5, 1), 3, 0))
+    assert torch.isnan(n.x[3]).all() and torch.isnan(n.h[3]).all() and int(torch.isnan(n.x).sum()) == H
+    # the bf16 gradients of y and of bf16 parameters
+    o = dict(weight=w.to(BF), y_norm=True, y_weight=w.to(BF), gate=w[None].to(BF))
+    q = ep.block_norm_backward(x, y, grad_x=bad, grad_h=y, **o)
+    assert torch.isnan(q.y[2]).all() and torch.isnan(q.y_weight[7]) and torch.isnan(q.gate[0, 7])
+    assert torch.isfinite(q.y[live].float()).all() and torch.isfinite(q.x[live]).all()
+    q = ep.block_norm_backward(bad, y, grad_x=x, grad_h=y, **o)
+    assert torch.isnan(q.x[2]).all() and torch.isnan(q.y[2]).all() and torch.isnan(q.weight).all()
+    q = ep.block_norm_backward(x, y, grad_x=bad, norm=False, gate=_randn(g, 5, 1).to(BF))
+    assert torch.isnan(q.gate[2, 0]) and torch.isfinite(q.gate[live].float()).all()
