@@ -275,13 +275,12 @@ _KINDS = {}
 
 
 def _kinds():
-    """Element types the library accepts, by the C type it reads."""
+    """Element types the library accepts, by the C type it reads (those that this torch has)."""
     if not _KINDS:
         import torch
-        _KINDS.update(bf16=(torch.bfloat16,), fp8=(torch.float8_e4m3fn, torch.uint8),
-                      f32=(torch.float32,), i64=(torch.int64,), i32=(torch.int32,),
-                      u8=(torch.uint8,), fp4=(torch.uint8, torch.float4_e2m1fn_x2),
-                      e8m0=(torch.float8_e8m0fnu, torch.uint8))
+        names = dict(bf16="bfloat16", fp8="float8_e4m3fn uint8", f32="float32", i64="int64", i32="int32", u8="uint8",
+                     fp4="uint8 float4_e2m1fn_x2", e8m0="float8_e8m0fnu uint8")
+        _KINDS.update({k: tuple(getattr(torch, n) for n in v.split() if hasattr(torch, n)) for k, v in names.items()})
     return _KINDS
 
 
