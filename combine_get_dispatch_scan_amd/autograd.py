@@ -94,6 +94,13 @@ def _first_order(backward):
     return run
 
 
+def _gradient(grad):
+    """An incoming gradient as the kernels read it: dense, from a 16-byte boundary (autograd
+    hands on views at any offset, a part of a larger tensor's gradient for one)."""
+    grad = grad.contiguous()
+    return grad if grad.data_ptr() % 16 == 0 else grad.clone()
+
+
 class _Routing:
     """The layout of one dispatch; `handle` is set once dispatch has run."""
 
@@ -114,7 +121,7 @@ class _Dispatch(torch.autograd.Function):
     @staticmethod
     @_first_order
     def backward(ctx, grad_recv):
-        return _dispatch_backward(grad_recv.contiguous(), ctx.handle), None, None, None
+        return _dispatch_backward(_gradient(grad_recv), ctx.handle), None, None, None
 
 
 def _unmapped_rows_zeroed(y, handle):
@@ -147,7 +154,7 @@ class _Combine(torch.autograd.Function):
         y, w = ctx.saved_tensors
         want_w = w is not None and ctx.needs_input_grad[1]
         grad_y = _unmapped_rows_zeroed(y, ctx.handle)
-        gy, gw = _combine_backward(grad_out.contiguous(), ctx.handle,
+        gy, gw = _combine_backward(_gradient(grad_out), ctx.handle,
                                    y=y.detach().contiguous() if want_w else None,
                                    topk_weights=w.detach().contiguous() if w is not None else None,
                                    grad_y=grad_y)
@@ -237,7 +244,7 @@ class _Experts(torch.autograd.Function):
         h = ctx.handle
         want_x, want_w, want_1, want_2 = ctx.needs_input_grad[:4]
         # with dispatch's copy of the weights
-        gy, gw = _combine_backward(grad_out.contiguous(), h, y=y2 if want_w else None)
+        gy, gw = _combine_backward(_gradient(grad_out), h, y=y2 if want_w else None)
         gx = g1 = g2 = None
         if want_2:
             g2 = grouped_wgrad_fp8(gy, a8, a_s, h, out_dtype=ctx.dtypes[1])
@@ -290,8 +297,8 @@ class _BlockNorm(torch.autograd.Function):
         _eager_only("the backward pass of block_norm")
         need = [n for n, wanted in zip(_NORM_INPUTS, ctx.needs_input_grad) if wanted]
         inputs = {n: None if t is None else t.detach() for n, t in zip(_NORM_INPUTS, ctx.saved_tensors)}
-        g = _block_norm_backward(grad_x=None if grad_x is None else grad_x.contiguous(),
-                                 grad_h=None if grad_h is None else grad_h.contiguous(),
+        g = _block_norm_backward(grad_x=None if grad_x is None else _gradient(grad_x),
+                                 grad_h=None if grad_h is None else _gradient(grad_h),
                                  need=need, **inputs, **ctx.options)
         return (*(getattr(g, n) for n in _NORM_INPUTS), None)
 

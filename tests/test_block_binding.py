@@ -21,3 +21,27 @@ def test_types_that_torch_lacks_concern_their_own_calls_only(monkeypatch, missin
 def test_types_of_this_torch():
     assert ep._kinds()["fp4"] == (torch.uint8, torch.float4_e2m1fn_x2)
     assert ep._kinds()["e8m0"] == (torch.float8_e8m0fnu, torch.uint8)
+
+
+def test_gradients_at_odd_offsets(monkeypatch):
+    """Outputs joined with something of an odd length hand back gradients that are dense and begin anywhere."""
+    import contextlib
+    import combine_get_dispatch_scan_amd.autograd as A
+    got = []
+
+    def backward(x, y=None, *, grad_x, grad_h, need, **o):
+        got.append([None if t is None else (t.is_contiguous() and t.data_ptr() % 16 == 0, t.clone()) for t in (grad_x, grad_h)])
+        return ep.BlockNormGrads(x=torch.zeros_like(x), y=torch.zeros_like(y))
+
+    monkeypatch.setattr(A, "_on", lambda *t: contextlib.nullcontext())
+    monkeypatch.setattr(A, "_eager_only", lambda what: None)
+    monkeypatch.setattr(A, "_block_norm_call", lambda x, y, **o: ep.BlockNorm(x + y, (x + y).bfloat16()))
+    monkeypatch.setattr(A, "_block_norm_backward", backward)
+    x, y = (torch.randn(4, 16).bfloat16().requires_grad_() for _ in range(2))
+    for first in (1, 3, 8):
+        n = A.block_norm(x, y)
+        g = torch.randn(first + 128).bfloat16()
+        torch.cat([torch.ones(first).bfloat16(), n.x.flatten(), n.h.flatten()]).backward(g)
+        (x_fits, gx), (h_fits, gh) = got.pop()
+        assert x_fits and h_fits
+        assert torch.equal(gx.flatten(), g[first:first + 64]) and torch.equal(gh.flatten(), g[first + 64:])

@@ -66,3 +66,46 @@ def test_block_norm_keeps_every_nan(ep, bits, H):
     assert torch.isnan(q.x[2]).all() and torch.isnan(q.y[2]).all() and torch.isnan(q.weight).all()
     q = ep.block_norm_backward(x, y, grad_x=bad, norm=False, gate=_randn(g, 5, 1).to(BF))
     assert torch.isnan(q.gate[2, 0]) and torch.isfinite(q.gate[live].float()).all()
+
+
+def test_autograd_of_gradients_at_odd_offsets(ep):
+    """Outputs joined with something of an odd length: their gradients are dense and begin anywhere."""
+    import combine_get_dispatch_scan_amd.autograd as A
+    T, H, E, I = 24, 256, 4, 128
+    g = _gen(5)
+    w1, w2 = _randn(g, E, 2 * I, H) * 0.1, _randn(g, E, H, I) * 0.1
+    idx = torch.stack([torch.randperm(E, generator=g, device=_dev())[:2] for _ in range(T)])
+    start = torch.ones(1, dtype=BF, device=_dev())
+
+    def grads(f, go, *leaves):
+        leaves = [t.clone().requires_grad_() for t in leaves]
+        got = []
+        for odd in (False, True):
+            outs = f(*leaves)
+            if odd:
+                torch.cat([start, *(o.flatten() for o in outs)]).backward(torch.cat([start, *(t.flatten() for t in go)]))
+            else:
+                torch.autograd.backward(outs, go)
+            got.append([t.grad for t in leaves])
+            for t in leaves:
+                t.grad = None
+        for a, b in zip(*got):
+            assert a.any() and torch.equal(a, b)
+
+    x, y = _randn(g, T, H).to(BF), _randn(g, T, H).to(BF)
+    go = [_randn(g, T, H).to(BF) for _ in range(2)]
+
+    def norm(x, y):
+        n = A.block_norm(x, y, y_norm=True)
+        return n.x, n.h
+
+    grads(norm, go, x, y)
+    wt = torch.rand(T, 2, generator=g, device=_dev()) + 0.1
+    grads(lambda x, wt, w1, w2: [A.experts(x, idx, wt, w1, w2)], go[:1], x, wt, w1, w2)
+
+    def there_and_back(x, wt):
+        recv, h = A.dispatch(x, idx, wt.detach(), E, 1)
+        return [A.combine(recv, h, wt)]
+
+    grads(there_and_back, go[:1], x, wt)
+    grads(lambda x: [A.dispatch(x, idx, wt, E, 1)[0]], [_randn(g, 2 * T, H).to(BF)], x)
