@@ -167,6 +167,14 @@ def _empty(t, dtype=None):
     return torch.empty_like(t, dtype=dtype, memory_format=torch.contiguous_format)
 
 
+def _written(t):
+    """Tells autograd that a call wrote into a tensor of the caller's, as torch's own in-place
+    operations do: a backward pass that kept it raises instead of reading the new values."""
+    import torch
+    if not t.is_inference():
+        torch.autograd.graph.increment_version(t)
+
+
 def _at(t):
     """Address of a tensor that the call itself made."""
     return None if t is None else t.data_ptr()
@@ -205,12 +213,14 @@ def block_norm(x, y=None, *, norm: bool = True, weight=None, y_norm: bool = Fals
                              weight_offset)
         if quantize and not norm:
             raise ValueError("quantize needs norm")
+        given = False
         if x_out is not None:
             if y is None:
                 raise ValueError("x_out needs y: without it x' is x")
             _shape(x_out, (T, H), "x_out")
             if x_out.dtype is not x.dtype:
                 raise TypeError(f"x_out must be {x.dtype}, got {x_out.dtype}")
+            given = True
         elif y is not None:
             x_out = _empty(x)
         h = codes = scales = None
@@ -221,6 +231,8 @@ def block_norm(x, y=None, *, norm: bool = True, weight=None, y_norm: bool = Fals
             scales = torch.empty_strided((T, H // 128), (H // 128, 1), dtype=torch.float32, device=x.device)
         _check(ep_block_norm(a, _ptr(x_out, None, "x_out"), _at(h), _at(codes) if T else None,
                              _at(scales) if T else None, _stream(x)))
+        if given:
+            _written(x_out)
     return BlockNorm(x if y is None else x_out, h, codes, scales)
 
 
@@ -351,11 +363,14 @@ def grouped_gemm_fp4(x, x_scales, w, w_scales, groups, *, group_stride: int = 0,
         args, expected = _group_args(groups, group_stride, x)
         if args[1] != G:
             raise ValueError(f"w holds {G} groups, the rows {args[1]}")
-        if out is None:
+        given = out is not None
+        if not given:
             out = torch.empty((rows, N), dtype=torch.bfloat16, device=x.device)
         elif out.shape != (rows, N):
             _shape(out, (rows, N), "out")
         _check(ep_grouped_gemm_fp4(_ptr(x, "fp8", "x"), _ptr(x_scales, "f32", "x_scales"), ld,
                                    _ptr(w, "fp4", "w"), _ptr(w_scales, "e8m0", "w_scales"), *args, rows, N, K,
                                    expected_rows or expected, _ptr(out, "bf16", "out"), _stream(x)))
+        if given:
+            _written(out)
     return out

@@ -109,3 +109,38 @@ def test_autograd_of_gradients_at_odd_offsets(ep):
 
     grads(there_and_back, go[:1], x, wt)
     grads(lambda x: [A.dispatch(x, idx, wt, E, 1)[0]], [_randn(g, 2 * T, H).to(BF)], x)
+
+
+def test_tensors_of_the_caller_that_are_written_count_as_changed(ep):
+    """A stream updated in place and a product's reused buffer, while a backward pass still needs what they held."""
+    import combine_get_dispatch_scan_amd.autograd as A
+    g = _gen(6)
+    x, y = _randn(g, 8, 256).to(BF), _randn(g, 8, 256).to(BF)
+    w = _randn(g, 256).requires_grad_()
+    q = ep.quantize_weights_fp4(_randn(g, 1, 256, 256))
+    x8, xs, off = _randn(g, 8, 256).to(torch.float8_e4m3fn), torch.ones(8, 2, device=_dev()), torch.tensor([0, 8], dtype=torch.int32, device=_dev())
+
+    def in_place():
+        ep.block_norm(x, y, x_out=x)
+
+    def reused():
+        ep.grouped_gemm_fp4(x8, xs, q.codes, q.scales, off, out=y)
+
+    for change in (in_place, reused):
+        n = A.block_norm(x, y, weight=w)
+        change()
+        with pytest.raises(RuntimeError, match="inplace"):
+            n.h.sum().backward()
+        n = A.block_norm(x, y, weight=w)
+        before = x._version, y._version
+        ep.block_norm(x, y)
+        ep.grouped_gemm_fp4(x8, xs, q.codes, q.scales, off)
+        assert before == (x._version, y._version)
+        n.h.sum().backward()
+    with torch.inference_mode():          # such tensors have no counter
+        a = x.clone()
+        want = ep.block_norm(x, y)
+        n = ep.block_norm(a, y, x_out=a)
+        assert n.x is a and torch.equal(a, want.x)
+        out = torch.empty(8, 256, dtype=BF, device=_dev())
+        assert ep.grouped_gemm_fp4(x8, xs, q.codes, q.scales, off, out=out) is out
