@@ -144,3 +144,30 @@ def test_tensors_of_the_caller_that_are_written_count_as_changed(ep):
         assert n.x is a and torch.equal(a, want.x)
         out = torch.empty(8, 256, dtype=BF, device=_dev())
         assert ep.grouped_gemm_fp4(x8, xs, q.codes, q.scales, off, out=out) is out
+
+
+# widths of the workgroup forms: one vector a lane, two, factors read again and sums in LDS, four vectors
+@pytest.mark.parametrize("H", [1032, 2048, 2056, 7168, 8200, 16384, 16392])
+@pytest.mark.parametrize("gate", ["token", "channel"])
+@pytest.mark.parametrize("xt", [BF, F32])
+def test_block_norm_of_many_rows_a_workgroup(ep, H, gate, xt):
+    """256 to 768 workgroups share 1700 rows, so each takes several and some one more than others: rows fetched ahead, the
+    slots that reductions use in turn, and the sums over a workgroup's rows; and up to twelve sums a share afterwards (256
+    workgroups with seven rows, or 768 with three: fewer roundings in all than the tolerance's depth counts)."""
+    o = _norm_case(H + 7, 1700, H, xt, F32 if gate == "token" else BF, gate=gate, gt=F32 if gate == "token" else BF)
+    _check_norm(ep, o, quantize=H % 128 == 0)
+    _check_norm_backward(ep, o, H)
+
+
+@pytest.mark.parametrize("H", [2048, 7168, 8320, 16512])
+def test_block_norm_alone_of_many_rows(ep, H):
+    for xt in (BF, F32):
+        o = _norm_case(H, 1300, H, xt, F32, y=False)
+        _check_norm(ep, o, quantize=True)
+        _check_norm_backward(ep, o, H)
+    o = _norm_case(H, 1300, H, y_norm=False, y_weight=False, gate="none")     # a plain residual addition
+    _check_norm(ep, o)
+    _check_norm_backward(ep, o, H)
+    o = _norm_case(H, 1300, H, weight=False, gate="channel", gt=F32)          # and no norm behind it
+    _check_norm(ep, o, norm=False)
+    _check_norm_backward(ep, o, H, norm=False)
