@@ -45,3 +45,14 @@ def test_gradients_at_odd_offsets(monkeypatch):
         (x_fits, gx), (h_fits, gh) = got.pop()
         assert x_fits and h_fits
         assert torch.equal(gx.flatten(), g[first:first + 64]) and torch.equal(gh.flatten(), g[first + 64:])
+
+
+@pytest.mark.parametrize("width,most", [(8, 512), (512, 512), (1024, 512), (1032, 768), (2048, 768), (2056, 512), (4096, 512),
+                                        (4104, 256), (7168, 256), (16384, 256), (16392, 256), (32768, 256)])
+def test_norm_workspace_of_every_team(width, most):
+    """Two sums of a row for each workgroup: at most three a CU (of 256) with one vector a lane, two with up to 256 threads,
+    else one; at least one where there are no rows."""
+    for rows in (0, 1, 5, 300, 1500, 1 << 20, 0x7FFFFF00):
+        teams = -(-rows // 4) if width <= 1024 else rows
+        want = max(1, min(teams, most)) * 2 * width * 4
+        assert ep.ep_block_norm_workspace_bytes(rows, width) == -(-want // 256) * 256
