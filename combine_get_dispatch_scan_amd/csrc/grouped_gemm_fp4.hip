@@ -647,9 +647,16 @@ hipError_t launch_grouped_gemm_fp4(const GemmFp4Launch& L, hipStream_t stream)
     if (KB <= kStreamWaves * B) {
         const int64_t room = kCus * (kStreamWaves / ((KB + B - 1) / B)), rounds = (tiles(16, kStreamCols) + room - 1) / room;
         const int64_t time = 800 + rounds * (250 + 20 * KB);
-        // at one or two rows a group its lead is small, but the model does not see it (81 us against 84 above); two
-        // blocks of K are too few for it (27 groups of two rows, 7680 x 256: 15.5 us, small 10.2)
-        if ((m <= 2 && KB > 2) || ((m <= 16 || rounds == 1) && time < small_time && time < large_time)) {
+        // at one or two rows a group its lead is small, but the model does not see it (81 us against 84 above).  Streamed,
+        // small form in us, two rows a group:
+        //   blocks of K  8 groups, N = 7680   27, 7680     64, 2048     256, 2048    256, 7680
+        //   1               5.6,  5.0          9.2, 10.7    6.6,  7.7   16.1, 25.1   38.5, 79.7
+        //   2               7.1,  5.3         14.4, 12.1    9.1,  8.2   25.5, 27.9   75.1, 92.0
+        //   3               6.5,  6.0         12.4, 15.5    8.2,  9.3   22.6, 32.5   92.5, 118
+        //   8               9.0,  8.7         22.7, 24.2   14.8, 16.4   47.7, 56.3    198, 215
+        //   16             14.2, 13.4         38.5, 40.5   24.9, 26.0    108, 111     379, 367
+        // At two blocks the better form changes with the size; there the model chooses (the better one of these, but at 64, 2048)
+        if ((m <= 2 && KB != 2) || ((m <= 16 || rounds == 1) && time < small_time && time < large_time)) {
             B == 4 ? stream_run<4>(L, stream) : stream_run<8>(L, stream);
             return hipGetLastError();
         }

@@ -5,6 +5,10 @@ Tolerances count roundings as in the checks of the products beside them: seven o
 neighbouring products may lose 2^-13 of the largest one, sums of fp32 2 u a term, bf16
 2^-8 of a value.
 """
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 
@@ -160,3 +164,27 @@ def test_product_fp4_whole_large_tiles_with_scales_at_any_offset(ep, shift):
     s = torch.empty(xs.numel() + 4, device=dev)[shift // 4:shift // 4 + xs.numel()].view(xs.shape).copy_(xs)
     assert b.data_ptr() % 16 == shift and s.data_ptr() % 16 == shift
     assert torch.equal(want, ep.grouped_gemm_fp4(x, s, codes, b, off, expected_rows=100000))
+
+
+_FORMS = r"""
+import torch
+import combine_get_dispatch_scan_amd as ep
+for K in (128, 256, 384):
+    for G, N in ((27, 7680), (256, 7680)):
+        x = torch.ones(G, K, device="cuda").to(torch.float8_e4m3fn)
+        w, s = (torch.zeros(G, N, K // n, device="cuda", dtype=torch.uint8) for n in (2, 32))
+        off = torch.arange(0, G + 1, device="cuda", dtype=torch.int32)
+        ep.grouped_gemm_fp4(x, torch.ones(G, K // 128, device="cuda"), w, s, off)
+        torch.cuda.synchronize()
+"""
+
+
+def test_form_of_short_rows(ep):
+    """One row a group: one block of K is streamed (256 groups, N = 7680: 38 us, 80 from small tiles), two go by the size.
+    EP_DEBUG is read once a process, hence another one."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", _FORMS], cwd=root, capture_output=True, text=True, timeout=100,
+                       env=dict(os.environ, EP_DEBUG="1"))
+    assert r.returncode == 0, r.stderr[-2000:]
+    got = [line.split()[1] for line in r.stderr.splitlines() if line.startswith("[moe_ep] grouped")]
+    assert got == ["grouped_gemm_fp4_" + n for n in ("stream", "stream", "small", "stream", "stream", "stream")]
