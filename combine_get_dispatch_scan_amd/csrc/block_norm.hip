@@ -19,7 +19,6 @@
 namespace moe_ep {
 
 constexpr int kTeamWaves = 16;               // waves of a row, at most
-constexpr int kCus = 256;
 constexpr int64_t kSmallBytes = (int64_t)16 << 20, kLargeBytes = (int64_t)256 << 20;
 
 template <int CTRL>

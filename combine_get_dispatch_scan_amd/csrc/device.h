@@ -7,6 +7,7 @@
 namespace moe_ep {
 
 constexpr int kWave = 64;
+constexpr int kXcds = 8, kCus = 256;
 constexpr int kChunk = 256;        // tokens per layout workgroup (4 waves)
 constexpr int kChunkWaves = kChunk / kWave;
 constexpr int kQBlock = 128;       // channels per FP8 scale

@@ -8,7 +8,6 @@
 
 namespace moe_ep {
 
-constexpr int kXcds = 8, kCus = 256;
 constexpr int kTile = 256;
 constexpr int kStage = kTile * kQBlock;
 

@@ -149,7 +149,7 @@ __device__ __forceinline__ void copy_stage(const TileSource& t, int kb, int wave
 
 __device__ __forceinline__ i32x8 read_w(const uint8_t* lds, int col0, int c, int lane)
 {
-    const int row = col0 + 32 * (c >> 1) + ((lane & 12) << 1) + (lane & 3) + 4 * (c & 1);
+    const int row = column_of(col0, c, lane);
     return read_fragment(lds + row * kQBlock, place_w(row), lane);
 }
 
