@@ -395,9 +395,10 @@ __global__ __launch_bounds__(THREADS) void block_norm_kernel(BlockNormLaunch L)
 //   dy = rz gt (g fy - z s / width)   (without y's norm: gt g fy)
 //   dweight = sum over rows of gh x' r;  S = sum over rows of gt g z, from which
 //   dy_weight = b * channel gate * S and the channel gate's gradient b (o + y_weight) S
-// The sums over rows stay in the registers of the workgroups (in LDS in rows of 8200 to
-// 16384: 4096 x 16384 323 us, 356 with registers, which spill), which take rows in a
-// fixed order, and are added by a second launch.  Stores go through the caches, unlike
+// The sums over rows stay in the registers of the workgroups, which take rows in a fixed
+// order, and are added by a second launch.  In rows of 8200 to 16384 they lie in LDS: 4096 x
+// 16384 325 us, 356 with registers; the row and its factors still spill some 30 to 50 of 128
+// registers there, and 300 to 360 in wider rows, whose sums are in registers again.  Stores go through the caches, unlike
 // forward ones: with readers of dx and dy behind them that is as fast or faster at every
 // size (8192 x 4096: 121 us, 134 around them).
 template <bool WAVE, int V, bool F32, int THREADS>
@@ -676,13 +677,14 @@ __global__ __launch_bounds__(kReduceThreads) void block_norm_reduce_kernel(Block
 
 // The team of a row: a wave with one or two vectors of eight a lane up to a width of
 // 1024, else a workgroup with one vector up to 2048, two up to 16384, then four.  In us
-// (16384 rows, bf16; forward, backward):
-//   1024: wave 26, 50; workgroup 33, 80      2048: one vector 52, 98; two 67, 105
-//   4096 (8192 rows): two vectors 50, 88; one 51, 114
+// (16384 rows, bf16, both norms, token gate; forward, backward):
+//   1024: wave 25, 51; workgroup 34, 63      2048: one vector 50, 86; two 53, 103
+//   4096: two vectors 94, 163; one 100, 190
 // From 8200 on a workgroup has up to 16 waves of 128 registers: factors are read again
-// (L2) and the next row is not fetched ahead.  4096 x 16384 takes 141 us forward, 323
-// backward (8 waves with four vectors each: 147, 388).  Beyond 16384 the backward pass
-// spills: 946 us for 2048 x 32768, 0.85 TB/s.
+// (L2) and the next row is not fetched ahead.  4096 x 16384 takes 134 us forward, 325
+// backward (8 waves with four vectors each: 147, 388).  Registers are spilled to memory by the
+// backward pass from 8200 on and by the forward pass beyond 16384 (21 and 37 of them): 2048 x
+// 32768 takes 156 us forward, 897 backward, 0.9 TB/s.
 struct Team {
     bool wave;
     int v, threads;
@@ -691,10 +693,11 @@ struct Team {
         const int64_t need = wave ? ((int64_t)rows + 3) / 4 : rows;
         return (int)(need < most ? need : most);
     }
-    // Workgroups a CU takes at once.  Forward, in us: 16384 x 4096 92 with two, 133 with one, 99 with four; 8191 x 2056
-    // (three waves) 40 with two, 31 with four.  Backward (waves of 120 registers with one vector, 210 with two):
-    // 16384 x 2048 87 with three, 98 with two; 16384 x 1024 50 with two, 59 with four; 8192 x 4096 88 with two, 112
-    // with one
+    // Workgroups a CU takes at once.  Forward, in us: 16384 x 4096 94 with two, 127 with one, 101 with four; 16384 x 2048
+    // 50 with four, 63 with two; 8191 x 2056 in fp32 (three waves) 43.6 with four, 44.1 with two, 34.9 and 35.9 with its
+    // inputs in the Infinity Cache.  Backward (waves of 120 registers with one vector, 210 with two): 16384 x 2048 86
+    // with three, 94 with two, 88 with four; 16384 x 1024 51 with two, 60 with four; 8192 x 4096 90 with two, 109 with
+    // one; 4096 x 16384 325 with one, 345 with two
     int forward_blocks(int rows) const { return blocks(rows, kCus * (v == 1 || wave || threads <= 192 ? 4 : 2)); }
     int backward_blocks(int rows) const { return blocks(rows, kCus * (!wave && v == 1 ? 3 : threads <= 256 ? 2 : 1)); }
 };

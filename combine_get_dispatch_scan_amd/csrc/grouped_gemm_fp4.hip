@@ -309,10 +309,10 @@ __device__ __forceinline__ void pair_tile(const GemmFp4Launch& a, int g, int m0,
 // the columns with each of the two blocks before.  The scales of four blocks are fetched
 // together: 16 bytes of a row of x, 16 of a column of w.
 //
-// 16384 rows in 32 equal groups, 4096 x 7168: 445 us, 2.2 PFLOP/s; 65536 rows 1680 us, 2.3 of
-// the 3.5 PFLOP/s that these instructions with the scaled sums reach from registers.  The
-// clock falls to 1.8 GHz, and the copies through L2 (1.2 ms without products) overlap the
-// products (1.3 ms without copies) in part.  Forms that came out slower there, by 1 to 40
+// 16384 rows in 32 equal groups, 4096 x 7168: 428-445 us, 2.2 PFLOP/s; 65536 rows 1640 us, 2.3
+// of the 3.5 PFLOP/s that these instructions with the scaled sums reach from registers.  The
+// clock falls to 1.8 GHz, and the copies through L2 (1.2 ms of the 65536 rows without products)
+// overlap the products (1.3 ms without copies) in part.  Forms that came out slower there, by 1 to 40
 // per cent: three buffers with copies two blocks ahead, the same with the two waves of a
 // SIMD taking turns between LDS and products, touching the lines of later blocks (each CU
 // all of its own, or its share of what the XCD reads), two workgroups a CU with 128 x 256
